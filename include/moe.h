@@ -69,6 +69,16 @@ extern "C" {
  * NVFP4 prefill runs on the BF16 matrix cores (see moe_prefill). */
 #define MOE_WTYPE_NVFP4 3
 
+/* INT4: 4-bit integers in groups of 32, 64 or 128 along K that share a BF16
+ * scale, value = scale (q - 8), q in 0..15; each matrix of the expert is a
+ * moe_q4 block without zero points (see moe_q4_layout).  The widespread
+ * group-quantised integer checkpoints hold their experts so.  moe_decode and
+ * moe_route_decode take it; moe_prefill, moe_route_decode_noalloc and the host
+ * expert kernel return MOE_EUNSUPPORTED. */
+#define MOE_WTYPE_INT4_G32 4
+#define MOE_WTYPE_INT4_G64 5
+#define MOE_WTYPE_INT4_G128 6
+
 /* Layer description.  hidden (H) and inter (I) must be multiples of 32
  * (MXFP4 blocks) and of 8 (BF16 16-byte vectors); 1 <= top_k <= n_experts
  * <= 1024. */
@@ -79,7 +89,8 @@ typedef struct moe_desc {
   int32_t top_k;        /* k: experts per token                              */
   int32_t has_shared;   /* 1: a shared expert also runs on every token, w=1  */
   int32_t renorm_topk;  /* 1: divide the k gate weights by their sum         */
-  int32_t wtype;        /* expert weights: MOE_WTYPE_BF16, _MXFP4 or _NVFP4  */
+  int32_t wtype;        /* expert weights: MOE_WTYPE_BF16, _MXFP4, _NVFP4 or
+                           _INT4_G32 / _G64 / _G128                          */
   int32_t router_wtype; /* router weights: MOE_WTYPE_F32 or MOE_WTYPE_BF16   */
 } moe_desc;
 
@@ -94,13 +105,18 @@ typedef struct moe_desc {
  *          [4] down codes [H][I/2], [5] down scales [H][I/32].
  *   NVFP4: as MXFP4 with scales [rows][K/16] (E4M3), followed at offset
  *          offsets[5] + H*I/16 by the fp32 scales of gate, up and down.
+ *   INT4 : [0] gate codes, [1] gate scales, [2] up codes, [3] up scales,
+ *          [4] down codes, [5] down scales, each pair a moe_q4 block.
  * Section offsets are 16-byte aligned; *bytes is a multiple of 256.
  * moe_pack_expert writes this layout.
  * Returns MOE_EINVAL for a bad descriptor. */
 int moe_expert_layout(const moe_desc* desc, size_t offsets[6], size_t* bytes);
 
 /* Workspace bytes a call needs (0 if none).  mode: 0 = moe_route,
- * 1 = moe_decode / moe_route_decode, 2 = moe_prefill, for T tokens.  Returns
+ * 1 = moe_decode / moe_route_decode, 2 = moe_prefill, 3 = moe_gate, 4 =
+ * moe_router_backward, for T tokens.  Modes 2 to 4 need no initial contents.
+ * A decode workspace that INT4 experts have used must be zeroed again before
+ * experts of another type use it.  Returns
  * 0 and sets the error text for an invalid descriptor or T.  A route
  * workspace starts with a 256-byte counter header that must be zero before
  * its first use; every call leaves it zero again.  A decode workspace must be
@@ -115,6 +131,8 @@ int moe_expert_layout(const moe_desc* desc, size_t offsets[6], size_t* bytes);
 #define MOE_MODE_ROUTE 0
 #define MOE_MODE_DECODE 1
 #define MOE_MODE_PREFILL 2
+#define MOE_MODE_GATE 3
+#define MOE_MODE_ROUTER_BACKWARD 4
 size_t moe_workspace_bytes(const moe_desc* desc, int32_t T, int32_t mode);
 
 /* Largest T moe_decode accepts (larger batches go through moe_prefill). */
@@ -137,6 +155,78 @@ int moe_route(const moe_desc* desc, const void* x, const void* w_router,
               int32_t T, int32_t* ids, float* w, void* ws, size_t ws_bytes,
               void* stream);
 
+/* ---- training of the router -------------------------------------------- */
+/* The router's steps as operators of their own, with their gradients:
+ * logits (moe_router_logits), the gate on them with the tokens each expert
+ * got and a balance loss (moe_gate), and back: moe_gate_backward gives the
+ * gradient of the logits, moe_router_backward that of the tokens and of the
+ * router's weights.  Experts are not differentiated here: dw, the gradient of
+ * the gate weights, comes from the caller (dw[t][j] is the gradient of y[t]
+ * dotted with the expert's output).  Only hidden, n_experts, top_k,
+ * renorm_topk and router_wtype of the descriptor are used. */
+
+/* moe_router_logits: logits[t][e] = sum over h of x[t][h] w_router[e][h], fp32
+ * accumulation.  x device [T][H] BF16, w_router device [E][H] in
+ * desc->router_wtype, logits device out [T][E] float; all 16-byte aligned. */
+int moe_router_logits(const moe_desc* desc, const void* x, const void* w_router,
+                      int32_t T, float* logits, void* stream);
+
+/* moe_gate: p = softmax(logits[t]) over the E experts, ids = the top_k experts
+ * by logit in descending order (ties to the lower id), w = p[ids] (divided by
+ * their sum if renorm_topk), and over the routed tokens
+ *   counts[e] = the number of (t, j) with ids[t][j] = e,  counts[E] = n, the
+ *               number of routed tokens
+ *   loss      = E / (k n^2) sum_e counts[e] sum_t p[t][e]   (0 for n = 0)
+ * i.e. E times the sum over experts of the share of choices that an expert got
+ * times its mean probability: 1 for a uniform router, up to E.
+ *   logits device [T][E] float
+ *   mask   device [T] bytes, 0 = padding, not routed; NULL = all are
+ *   ids    device out [T][k] int32,  w device out [T][k] float
+ *   counts device out [E + 1] int32 or NULL,  loss device out [1] float or NULL
+ *   ws     moe_workspace_bytes(.., MOE_MODE_GATE); not used (may be NULL) when
+ *          counts and loss are both NULL
+ * A logit of -inf means that the expert is not available to the token: it is
+ * never chosen; where fewer than k are left the remaining ids are -1 with w 0.
+ * A token that is masked, or has no expert left, is not routed: all its ids
+ * are -1 (which moe_decode and moe_prefill skip) and its w are 0.  A NaN is
+ * never chosen, and a row that holds a NaN or +inf has w = NaN (a row of NaN
+ * only: ids -1) and makes the loss NaN.  The sums are taken in a fixed order:
+ * equal calls give equal bits.  T >= 0 (T == 0: counts and loss are set to 0). */
+int moe_gate(const moe_desc* desc, const float* logits, int32_t T,
+             const uint8_t* mask, int32_t* ids, float* w, int32_t* counts,
+             float* loss, void* ws, size_t ws_bytes, void* stream);
+
+/* moe_gate_backward: dlogits = the gradient of (sum of dw * w) + dloss * loss
+ * into the logits.  counts are constants of the loss (the choice itself has no
+ * gradient).  logits, ids, w, counts as moe_gate gave them:
+ *   dw      device [T][k] float or NULL (no gradient comes through w; w may
+ *           then be NULL too)
+ *   dloss   device [1] float or NULL (none through the loss; counts may then be
+ *           NULL too)
+ *   dlogits device out [T][E] float, overwritten (0 for tokens that are not
+ *           routed: those whose first id is negative); may be logits itself
+ * ids outside [0, E) take no gradient. */
+int moe_gate_backward(const moe_desc* desc, const float* logits, int32_t T,
+                      const int32_t* ids, const float* w, const float* dw,
+                      const int32_t* counts, const float* dloss, float* dlogits,
+                      void* stream);
+
+/* moe_router_backward: dx = dlogits w_router (BF16, rounded once from fp32)
+ * and dw_router = dlogits^T x (fp32), on the BF16 matrix cores with dlogits
+ * (and an fp32 w_router) entering as two BF16 parts each, i.e. to within
+ * 2^-17.  Sums over tokens are taken in a fixed order.
+ *   x         device [T][H] BF16 (may be NULL without dw_router)
+ *   w_router  device [E][H] in desc->router_wtype (may be NULL without dx)
+ *   dlogits   device [T][E] float
+ *   dx        device out [T][H] BF16 or NULL
+ *   dw_router device out [E][H] float or NULL, overwritten
+ *   ws        moe_workspace_bytes(.., MOE_MODE_ROUTER_BACKWARD)
+ * All 16-byte aligned.  0 <= T <= 2^20 (T == 0: dw_router is set to 0). */
+int moe_router_backward(const moe_desc* desc, const void* x, const void* w_router,
+                        int32_t T, const float* dlogits, void* dx,
+                        float* dw_router, void* ws, size_t ws_bytes,
+                        void* stream);
+
 /* ---- expert FFNs + weighted combine ------------------------------------ */
 /* moe_decode: y[t] = sum over j of w[t][j] * FFN_{ids[t][j]}(x[t])
  *                    (+ FFN_shared(x[t]) when desc->has_shared),
@@ -158,7 +248,9 @@ int moe_route(const moe_desc* desc, const void* x, const void* w_router,
  * matrix core by cost: an expert's rows weigh more the more tokens chose
  * it) and each row's gate-weighted result is added into y with an fp32
  * atomic, so the summation order (and the last bits of y) can differ
- * between runs.
+ * between runs.  INT4 experts: x as given, h held as two BF16 parts (to within
+ * 2^-17), fp32 accumulation, two kernels for any T, T * k <= 512, the sums in
+ * a fixed order (no atomics on y, no wait between workgroups).
  *   x              device [T][H] BF16;   1 <= T <= MOE_DECODE_MAX_T
  *   ids, w         device [T][k] (from moe_route or the caller)
  *   slot_of_expert device [E] int32: slot holding expert e, -1 = not
@@ -288,10 +380,67 @@ int moe_quantize_mxfp4(const float* src, int32_t rows, int32_t K,
  * (device, row-major, src_type MOE_WTYPE_F32 or MOE_WTYPE_BF16).  BF16
  * experts: values rounded to BF16 (nearest even) if given as fp32.  MXFP4
  * experts: quantised with the encoder of moe_quantize_mxfp4 (blocks along
- * K = H for gate/up, K = I for down).  Host and device blocks share this
+ * K = H for gate/up, K = I for down).  INT4 experts: as moe_q4_quantize
+ * without zero points.  Host and device blocks share this
  * layout, so the same bytes serve the pinned pool and the slots. */
 int moe_pack_expert(const moe_desc* desc, const void* gate, const void* up,
                     const void* down, int32_t src_type, void* dst, void* stream);
+
+/* ---- 4-bit integer matrices -------------------------------------------- */
+/* A matrix [rows][cols] of 4-bit integers q in 0..15 with a BF16 scale, and
+ * with has_zero a zero point byte, per group of 32, 64 or 128 columns of a
+ * row: value = scale (q - zero), zero = 8 without has_zero.  rows and cols are
+ * free (rows <= 2^24, cols <= 2^20). */
+typedef struct moe_q4_desc {
+  int32_t rows;      /* N: outputs                                           */
+  int32_t cols;      /* K: inputs                                            */
+  int32_t group;     /* columns per scale: 32, 64 or 128                     */
+  int32_t has_zero;  /* 1: a zero point per group                            */
+} moe_q4_desc;
+
+/* moe_q4_layout: the block of a matrix, laid out for the matrix cores.  Rows
+ * are padded to 16 and columns to 128 (padding has scale 0).
+ *   offsets[0] codes: [row tiles of 16][column blocks of 128] tiles of 1 KB.
+ *              Lane l = 16 q + r of a tile has bytes 16 l .. 16 l + 15: row r;
+ *              dword s of them the columns 32 s + 8 q + (0..7), element i in
+ *              nibble i / 2 + 4 (i % 2) of the dword.
+ *   offsets[1] scales: BF16 [row tiles][groups][16 rows]
+ *   offsets[2] zero points: bytes, same order (0 without has_zero)
+ * A block starts 16-byte aligned. */
+int moe_q4_layout(const moe_q4_desc* desc, size_t offsets[3], size_t* bytes);
+
+/* moe_q4_quantize: a float matrix into its block (dst, device, 16-byte
+ * aligned, moe_q4_layout bytes).  src device [rows][cols], rows src_ld
+ * elements apart, src_type MOE_WTYPE_F32 or MOE_WTYPE_BF16.  Per group:
+ * without zero points scale = max|v| / 7; with them scale = (hi - lo) / 15
+ * with hi = max(v, 0), lo = min(v, 0), zero = -lo / scale rounded.  The scale
+ * is rounded to BF16, then q = v / scale + zero rounded to the nearest (ties
+ * to even) and clamped to 0..15. */
+int moe_q4_quantize(const moe_q4_desc* desc, const void* src, int32_t src_type,
+                    int64_t src_ld, void* dst, void* stream);
+
+/* moe_q4_pack: an already quantised matrix into its block, its values
+ * unchanged.  codes device [rows][ceil(cols / 2)] (element 2j in the low
+ * nibble of byte j), scales device BF16 [rows][ceil(cols / group)], zeros
+ * device bytes of the same shape (0..240; with has_zero only, else NULL).
+ * The matrices of an INT4 expert are packed one by one at the expert's
+ * offsets[0], [2] and [4]. */
+int moe_q4_pack(const moe_q4_desc* desc, const uint8_t* codes, const void* scales,
+                const uint8_t* zeros, void* dst, void* stream);
+
+/* moe_q4_linear: y[t][n] = sum over k of x[t][k] W[n][k], x BF16 as given,
+ * fp32 accumulation in a fixed order.  Made for the few tokens of a decode
+ * step; beyond 64 tokens the matrix is read again for every 64.
+ *   x     device BF16 [T][cols], rows x_ld elements apart (fastest with cols
+ *         and x_ld multiples of 8 and x 16-byte aligned)
+ *   block device, moe_q4_layout's
+ *   y     device out [T][rows], rows y_ld elements apart, y_type
+ *         MOE_WTYPE_F32 or MOE_WTYPE_BF16 (rounded once); must not overlap x
+ * 0 <= T <= 65536.  x is taken to be below 2^120 in magnitude: an infinity in
+ * a token makes that token's whole y NaN. */
+int moe_q4_linear(const moe_q4_desc* desc, const void* x, int64_t x_ld, int32_t T,
+                  const void* block, void* y, int32_t y_type, int64_t y_ld,
+                  void* stream);
 
 /* moe_debug_dequant_mxfp4: n_blocks MXFP4 blocks (codes 16 B each, one scale
  * byte each) -> 32 * n_blocks floats, value e2m1(code) * 2^(s-127) computed

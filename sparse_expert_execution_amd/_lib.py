@@ -21,10 +21,15 @@ WTYPE_F32 = 0
 WTYPE_BF16 = 1
 WTYPE_MXFP4 = 2
 WTYPE_NVFP4 = 3
+WTYPE_INT4_G32 = 4
+WTYPE_INT4_G64 = 5
+WTYPE_INT4_G128 = 6
 
 MODE_ROUTE = 0
 MODE_DECODE = 1
 MODE_PREFILL = 2
+MODE_GATE = 3
+MODE_ROUTER_BACKWARD = 4
 
 DECODE_MAX_T = 64
 NOALLOC_SCRATCH_BYTES = 8 << 20
@@ -43,6 +48,8 @@ EXPORTS = (
     "moe_cache_create", "moe_cache_destroy", "moe_cache_set_bandwidths",
     "moe_cache_plan", "cache_fill", "moe_cache_release",
     "moe_cache_debug_fail_fills", "moe_cache_planner", "moe_probe_bandwidths",
+    "moe_router_logits", "moe_gate", "moe_gate_backward", "moe_router_backward",
+    "moe_q4_layout", "moe_q4_quantize", "moe_q4_pack", "moe_q4_linear",
     "moe_host_experts", "moe_host_expert_rate", "moe_last_error", "moe_abi_version",
 )
 
@@ -52,6 +59,11 @@ class MoeDesc(ctypes.Structure):
                 ("n_experts", ctypes.c_int32), ("top_k", ctypes.c_int32),
                 ("has_shared", ctypes.c_int32), ("renorm_topk", ctypes.c_int32),
                 ("wtype", ctypes.c_int32), ("router_wtype", ctypes.c_int32)]
+
+
+class MoeQ4Desc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("cols", ctypes.c_int32),
+                ("group", ctypes.c_int32), ("has_zero", ctypes.c_int32)]
 
 
 _I32xP = ctypes.c_int32 * PLAN_MAX
@@ -90,6 +102,7 @@ def lib():
                           ctypes.c_size_t, ctypes.c_double)
     DP = ctypes.POINTER(MoeDesc)
     PP = ctypes.POINTER(MoePlan)
+    QP = ctypes.POINTER(MoeQ4Desc)
     sig = {
         "moe_expert_layout": (ctypes.c_int, [DP, ctypes.POINTER(SZ), ctypes.POINTER(SZ)]),
         "moe_workspace_bytes": (SZ, [DP, I32, I32]),
@@ -99,6 +112,14 @@ def lib():
         "moe_route_decode": (ctypes.c_int, [DP, P, P, I32, P, P, P, P, P, P, P, SZ, P]),
         "moe_route_decode_noalloc": (ctypes.c_int, [DP, P, P, I32, P, P, P, P, P, P, P, P]),
         "moe_decode_launch_tokens": (I32, [DP]),
+        "moe_router_logits": (ctypes.c_int, [DP, P, P, I32, P, P]),
+        "moe_gate": (ctypes.c_int, [DP, P, I32, P, P, P, P, P, P, SZ, P]),
+        "moe_gate_backward": (ctypes.c_int, [DP, P, I32, P, P, P, P, P, P, P]),
+        "moe_router_backward": (ctypes.c_int, [DP, P, P, I32, P, P, P, P, SZ, P]),
+        "moe_q4_layout": (ctypes.c_int, [QP, ctypes.POINTER(SZ), ctypes.POINTER(SZ)]),
+        "moe_q4_quantize": (ctypes.c_int, [QP, P, I32, I64, P, P]),
+        "moe_q4_pack": (ctypes.c_int, [QP, P, P, P, P, P]),
+        "moe_q4_linear": (ctypes.c_int, [QP, P, I64, I32, P, P, I32, I64, P]),
         "moe_merge_partials": (ctypes.c_int, [P, P, P, SZ, P]),
         "moe_quantize_mxfp4": (ctypes.c_int, [P, I32, I32, I64, P, P, P]),
         "moe_pack_expert": (ctypes.c_int, [DP, P, P, P, I32, P, P]),

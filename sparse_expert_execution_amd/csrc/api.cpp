@@ -83,6 +83,43 @@ RouteWs route_ws(const moe_desc* d, int T, bool decode) {
   return w;
 }
 
+// decode workspace of 4-bit integer experts: the header (the router's ticket
+// is its first word), logits z [T][E], the units' (entries, slot) and pair
+// lists, h of every pair and of the shared expert's tokens in two BF16 parts.
+struct Q4DecodeWs {
+  size_t z, units, lists, h_hi, h_lo, total;
+};
+Q4DecodeWs q4_decode_ws(const moe_desc* d, int T) {
+  Q4DecodeWs w;
+  const size_t P = (size_t)T * d->top_k, h = (P + T) * d->inter * 2;
+  size_t o = kDecodeHeader;
+  w.z = o; o = align_up(o + (size_t)T * d->n_experts * 4);
+  w.units = o; o = align_up(o + (P + 1) * 8);
+  w.lists = o; o = align_up(o + P * P * 2);
+  w.h_hi = o; o = align_up(o + h);
+  w.h_lo = o; o = align_up(o + h);
+  w.total = o;
+  return w;
+}
+
+constexpr int kMaxGradTokens = 1 << 20;   // moe_router_backward
+
+struct GateWs {
+  size_t ticket, share, n, s, c, total;
+};
+GateWs gate_ws(const moe_desc* d, int T) {
+  GateWs w;
+  const size_t parts = moe::gate_parts(T), row = parts * d->n_experts * 4;
+  size_t o = 0;
+  w.ticket = o; o = align_up(o + 4);
+  w.share = o; o = align_up(o + 16 * 4);
+  w.n = o; o = align_up(o + parts * 4);
+  w.s = o; o = align_up(o + row);
+  w.c = o; o = align_up(o + row);
+  w.total = o;
+  return w;
+}
+
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 hipStream_t as_stream(void* s) { return static_cast<hipStream_t>(s); }
@@ -98,9 +135,15 @@ size_t moe_workspace_bytes(const moe_desc* desc, int32_t T, int32_t mode) {
     case MOE_MODE_ROUTE:
       return route_ws(desc, T, false).total;
     case MOE_MODE_DECODE:
+      if (moe::q4_group(desc->wtype)) return q4_decode_ws(desc, T).total;
       return route_ws(desc, T, true).total;
     case MOE_MODE_PREFILL:
       return prefill_ws(desc, T).total;
+    case MOE_MODE_GATE:
+      return gate_ws(desc, T).total;
+    case MOE_MODE_ROUTER_BACKWARD:
+      if (T > kMaxGradTokens) { set_error(MOE_EUNSUPPORTED, "T %d above 2^20", T); return 0; }
+      return moe::router_backward_bytes(T, desc->hidden, desc->n_experts);
     default:
       set_error(MOE_EINVAL, "unknown mode %d", mode);
       return 0;
@@ -153,6 +196,45 @@ static int check_ffn_args(const moe_desc* desc, const void* x, int32_t T, const 
   return MOE_OK;
 }
 
+// decode of 4-bit integer experts: the router where asked for, then two launches
+static int q4_decode_impl(const moe_desc* desc, const void* x, const void* w_router, int32_t T,
+                          int32_t* ids, float* w, const int32_t* slot_of_expert,
+                          const void* slot_pool, const void* shared_expert, float* y, void* ws,
+                          size_t ws_bytes, void* stream) {
+  const Q4DecodeWs L = q4_decode_ws(desc, T);
+  if (!ws || ws_bytes < L.total || !aligned(ws, 256))
+    return set_error(MOE_EWORKSPACE, "decode workspace %zu < %zu bytes (or not 256-aligned)",
+                     ws_bytes, L.total);
+  uint8_t* b = static_cast<uint8_t*>(ws);
+  const char* name = w_router ? "moe_route_decode" : "moe_decode";
+  if (w_router) {
+    const int st = hip_status(
+        moe::launch_route_small(x, w_router, desc->router_wtype == MOE_WTYPE_F32, T, desc->hidden,
+                                desc->n_experts, desc->top_k, desc->renorm_topk,
+                                reinterpret_cast<float*>(b + L.z),
+                                reinterpret_cast<unsigned*>(b), ids, w, as_stream(stream)),
+        name);
+    if (st) return st;
+  }
+  size_t off[6], bytes;
+  layout(desc, off, &bytes);
+  moe::Q4Experts a;
+  a.x = static_cast<const uint16_t*>(x);
+  a.ids = ids; a.w = w; a.slot_of = slot_of_expert;
+  a.pool = static_cast<const uint8_t*>(slot_pool);
+  a.shared = static_cast<const uint8_t*>(shared_expert);
+  a.expert_bytes = (int64_t)bytes;
+  for (int i = 0; i < 6; ++i) a.off[i] = (int64_t)off[i];
+  a.T = T; a.H = desc->hidden; a.I = desc->inter; a.E = desc->n_experts; a.k = desc->top_k;
+  a.y = y;
+  a.units = reinterpret_cast<int2*>(b + L.units);
+  a.lists = reinterpret_cast<int16_t*>(b + L.lists);
+  a.h_hi = reinterpret_cast<uint16_t*>(b + L.h_hi);
+  a.h_lo = reinterpret_cast<uint16_t*>(b + L.h_lo);
+  return hip_status(moe::launch_q4_experts(a, moe::q4_group(desc->wtype), as_stream(stream)),
+                    name);
+}
+
 static int decode_impl(const moe_desc* desc, const void* x, const void* w_router, int32_t T,
                        int32_t* ids, float* w, const int32_t* slot_of_expert,
                        const void* slot_pool, const void* shared_expert, float* y, void* ws,
@@ -161,6 +243,9 @@ static int decode_impl(const moe_desc* desc, const void* x, const void* w_router
     return set_error(MOE_EUNSUPPORTED, "decode supports top_k <= 8 (got %d)", desc->top_k);
   if (T < 0 || T > MOE_DECODE_MAX_T || T * desc->top_k > 1024)
     return set_error(MOE_EINVAL, "decode T %d outside [1, %d] or T*k > 1024", T, MOE_DECODE_MAX_T);
+  if (moe::q4_group(desc->wtype))
+    return q4_decode_impl(desc, x, w_router, T, ids, w, slot_of_expert, slot_pool, shared_expert,
+                          y, ws, ws_bytes, stream);
   if (!moe::decode_shape_supported(desc->wtype, desc->hidden, desc->inter))
     return set_error(MOE_EUNSUPPORTED, "decode shape H=%d I=%d not compiled", desc->hidden,
                      desc->inter);
@@ -208,6 +293,7 @@ static int decode_impl(const moe_desc* desc, const void* x, const void* w_router
 int32_t moe_decode_launch_tokens(const moe_desc* desc) {
   const int st = check_desc(desc);
   if (st) return st;
+  if (moe::q4_group(desc->wtype)) return MOE_DECODE_MAX_T;   // never split
   if (!moe::decode_shape_supported(desc->wtype, desc->hidden, desc->inter))
     return set_error(MOE_EUNSUPPORTED, "decode shape H=%d I=%d not compiled", desc->hidden,
                      desc->inter);
@@ -344,6 +430,12 @@ int moe_pack_expert(const moe_desc* desc, const void* gate, const void* up, cons
       err = moe::launch_quantize_nvfp4(up, sb, I, H, b + off[2], b + off[3], gs + 1, s);
     if (err == hipSuccess)
       err = moe::launch_quantize_nvfp4(down, sb, H, I, b + off[4], b + off[5], gs + 2, s);
+  } else if (const int group = moe::q4_group(desc->wtype)) {
+    err = moe::launch_q4_quantize(gate, sb, I, H, H, group, b + off[0], b + off[1], nullptr, s);
+    if (err == hipSuccess)
+      err = moe::launch_q4_quantize(up, sb, I, H, H, group, b + off[2], b + off[3], nullptr, s);
+    if (err == hipSuccess)
+      err = moe::launch_q4_quantize(down, sb, H, I, I, group, b + off[4], b + off[5], nullptr, s);
   } else {
     err = moe::launch_quantize_mxfp4(gate, sb, I, H, H, b + off[0], b + off[1], s);
     if (err == hipSuccess)
@@ -412,6 +504,173 @@ int moe_debug_read_probe(const void* buf, size_t bytes, int32_t blocks, uint32_t
     return set_error(MOE_EINVAL, "bad read-probe arguments");
   return hip_status(moe::launch_read_probe(buf, bytes, blocks, out, as_stream(stream)),
                     "moe_debug_read_probe");
+}
+
+// ---- training of the router -------------------------------------------------
+int moe_router_logits(const moe_desc* desc, const void* x, const void* w_router, int32_t T,
+                      float* logits, void* stream) {
+  moe::ApiRange range_("moe_router_logits");
+  int st = check_desc(desc);
+  if (st) return st;
+  if (T == 0) return MOE_OK;
+  if (T < 0) return set_error(MOE_EINVAL, "T < 0");
+  if (!x || !w_router || !logits) return set_error(MOE_EINVAL, "null pointer");
+  if (!aligned(x, 16) || !aligned(w_router, 16) || !aligned(logits, 16))
+    return set_error(MOE_EINVAL, "x, w_router and logits must be 16-byte aligned");
+  return hip_status(moe::launch_logits(x, w_router, desc->router_wtype == MOE_WTYPE_F32, T,
+                                       desc->hidden, desc->n_experts, logits, as_stream(stream)),
+                    "moe_router_logits");
+}
+
+int moe_gate(const moe_desc* desc, const float* logits, int32_t T, const uint8_t* mask,
+             int32_t* ids, float* w, int32_t* counts, float* loss, void* ws, size_t ws_bytes,
+             void* stream) {
+  moe::ApiRange range_("moe_gate");
+  int st = check_desc(desc);
+  if (st) return st;
+  if (T < 0) return set_error(MOE_EINVAL, "T < 0");
+  if (T == 0) {                                       // no token: nothing chosen, no loss
+    if (counts)
+      st = hip_status(moe::launch_fill_i32(counts, 0, desc->n_experts + 1, as_stream(stream)),
+                      "moe_gate");
+    if (!st && loss)
+      st = hip_status(moe::launch_fill_i32(reinterpret_cast<int32_t*>(loss), 0, 1,
+                                           as_stream(stream)),
+                      "moe_gate");
+    return st;
+  }
+  if (!logits || !ids || !w) return set_error(MOE_EINVAL, "null pointer");
+  const GateWs L = gate_ws(desc, T);
+  if ((counts || loss) && (!ws || ws_bytes < L.total || !aligned(ws, 256)))
+    return set_error(MOE_EWORKSPACE, "gate workspace %zu < %zu bytes (or not 256-aligned)",
+                     ws_bytes, L.total);
+  uint8_t* b = static_cast<uint8_t*>(ws);
+  moe::GateArgs a = {};
+  a.z = logits; a.mask = mask; a.T = T; a.E = desc->n_experts; a.k = desc->top_k;
+  a.renorm = desc->renorm_topk; a.ids = ids; a.w = w; a.counts = counts; a.loss = loss;
+  if (counts || loss) {
+    a.part_s = reinterpret_cast<float*>(b + L.s);
+    a.part_c = reinterpret_cast<int32_t*>(b + L.c);
+    a.part_n = reinterpret_cast<int32_t*>(b + L.n);
+    a.share = reinterpret_cast<float*>(b + L.share);
+    a.ticket = reinterpret_cast<unsigned*>(b + L.ticket);
+  }
+  return hip_status(moe::launch_gate(a, as_stream(stream)), "moe_gate");
+}
+
+int moe_gate_backward(const moe_desc* desc, const float* logits, int32_t T, const int32_t* ids,
+                      const float* w, const float* dw, const int32_t* counts, const float* dloss,
+                      float* dlogits, void* stream) {
+  moe::ApiRange range_("moe_gate_backward");
+  int st = check_desc(desc);
+  if (st) return st;
+  if (T < 0) return set_error(MOE_EINVAL, "T < 0");
+  if (T == 0) return MOE_OK;
+  if (!logits || !ids || !dlogits) return set_error(MOE_EINVAL, "null pointer");
+  if (dw && !w) return set_error(MOE_EINVAL, "dw given without w");
+  if (dloss && !counts) return set_error(MOE_EINVAL, "dloss given without counts");
+  moe::GateBackward a;
+  a.z = logits; a.ids = ids; a.w = w; a.dw = dw; a.counts = counts; a.dloss = dloss;
+  a.T = T; a.E = desc->n_experts; a.k = desc->top_k; a.renorm = desc->renorm_topk; a.dz = dlogits;
+  return hip_status(moe::launch_gate_backward(a, as_stream(stream)), "moe_gate_backward");
+}
+
+int moe_router_backward(const moe_desc* desc, const void* x, const void* w_router, int32_t T,
+                        const float* dlogits, void* dx, float* dw_router, void* ws,
+                        size_t ws_bytes, void* stream) {
+  moe::ApiRange range_("moe_router_backward");
+  int st = check_desc(desc);
+  if (st) return st;
+  if (T < 0) return set_error(MOE_EINVAL, "T < 0");
+  if (T > kMaxGradTokens) return set_error(MOE_EUNSUPPORTED, "router backward T %d above 2^20", T);
+  if (!dx && !dw_router) return MOE_OK;
+  if (dw_router && !aligned(dw_router, 16))
+    return set_error(MOE_EINVAL, "dw_router must be 16-byte aligned");
+  if (T == 0)                                         // a sum over no token
+    return dw_router ? hip_status(moe::launch_fill_i32(reinterpret_cast<int32_t*>(dw_router), 0,
+                                                       (int64_t)desc->n_experts * desc->hidden,
+                                                       as_stream(stream)),
+                                  "moe_router_backward")
+                     : MOE_OK;
+  if (!dlogits || (dx && !w_router) || (dw_router && !x))
+    return set_error(MOE_EINVAL, "null pointer");
+  if (!aligned(dlogits, 16) || (dx && (!aligned(dx, 16) || !aligned(w_router, 16))) ||
+      (dw_router && !aligned(x, 16)))
+    return set_error(MOE_EINVAL, "x, w_router, dlogits and dx must be 16-byte aligned");
+  const size_t need = moe::router_backward_bytes(T, desc->hidden, desc->n_experts);
+  if (!ws || ws_bytes < need || !aligned(ws, 256))
+    return set_error(MOE_EWORKSPACE, "router backward workspace %zu < %zu bytes (or not "
+                     "256-aligned)", ws_bytes, need);
+  moe::RouterBackward a;
+  a.x = x; a.w = w_router; a.dz = dlogits; a.router_f32 = desc->router_wtype == MOE_WTYPE_F32;
+  a.T = T; a.H = desc->hidden; a.E = desc->n_experts;
+  a.dx = static_cast<uint16_t*>(dx); a.dw = dw_router; a.ws = static_cast<uint8_t*>(ws);
+  return hip_status(moe::launch_router_backward(a, as_stream(stream)), "moe_router_backward");
+}
+
+// ---- 4-bit integer matrices -------------------------------------------------
+int moe_q4_quantize(const moe_q4_desc* desc, const void* src, int32_t src_type, int64_t src_ld,
+                    void* dst, void* stream) {
+  moe::ApiRange range_("moe_q4_quantize");
+  int st = moe::check_q4(desc);
+  if (st) return st;
+  if (!src || !dst) return set_error(MOE_EINVAL, "null pointer");
+  if (src_type != MOE_WTYPE_F32 && src_type != MOE_WTYPE_BF16)
+    return set_error(MOE_EUNSUPPORTED, "source type %d not supported", src_type);
+  if (src_ld < desc->cols) return set_error(MOE_EINVAL, "src_ld below cols");
+  if (!aligned(dst, 16)) return set_error(MOE_EINVAL, "dst must be 16-byte aligned");
+  size_t off[3], bytes;
+  moe::q4_layout(desc->rows, desc->cols, desc->group, desc->has_zero != 0, off, &bytes);
+  uint8_t* b = static_cast<uint8_t*>(dst);
+  return hip_status(moe::launch_q4_quantize(src, src_type == MOE_WTYPE_BF16, desc->rows,
+                                            desc->cols, src_ld, desc->group, b + off[0],
+                                            b + off[1], desc->has_zero ? b + off[2] : nullptr,
+                                            as_stream(stream)),
+                    "moe_q4_quantize");
+}
+
+int moe_q4_pack(const moe_q4_desc* desc, const uint8_t* codes, const void* scales,
+                const uint8_t* zeros, void* dst, void* stream) {
+  moe::ApiRange range_("moe_q4_pack");
+  int st = moe::check_q4(desc);
+  if (st) return st;
+  if (!codes || !scales || !dst) return set_error(MOE_EINVAL, "null pointer");
+  if ((zeros != nullptr) != (desc->has_zero != 0))
+    return set_error(MOE_EINVAL, "zeros go with has_zero");
+  if (!aligned(dst, 16) || !aligned(scales, 2))
+    return set_error(MOE_EINVAL, "dst must be 16-byte and scales 2-byte aligned");
+  size_t off[3], bytes;
+  moe::q4_layout(desc->rows, desc->cols, desc->group, desc->has_zero != 0, off, &bytes);
+  uint8_t* b = static_cast<uint8_t*>(dst);
+  return hip_status(moe::launch_q4_pack(codes, static_cast<const uint16_t*>(scales), zeros,
+                                        desc->rows, desc->cols, desc->group, b + off[0],
+                                        b + off[1], desc->has_zero ? b + off[2] : nullptr,
+                                        as_stream(stream)),
+                    "moe_q4_pack");
+}
+
+int moe_q4_linear(const moe_q4_desc* desc, const void* x, int64_t x_ld, int32_t T,
+                  const void* block, void* y, int32_t y_type, int64_t y_ld, void* stream) {
+  moe::ApiRange range_("moe_q4_linear");
+  int st = moe::check_q4(desc);
+  if (st) return st;
+  if (T == 0) return MOE_OK;
+  if (T < 0 || T > 65536) return set_error(MOE_EINVAL, "T %d outside [0, 65536]", T);
+  if (!x || !block || !y) return set_error(MOE_EINVAL, "null pointer");
+  if (y_type != MOE_WTYPE_F32 && y_type != MOE_WTYPE_BF16)
+    return set_error(MOE_EUNSUPPORTED, "output type %d not supported", y_type);
+  if (x_ld < desc->cols || y_ld < desc->rows)
+    return set_error(MOE_EINVAL, "x_ld below cols or y_ld below rows");
+  if (!aligned(block, 16) || !aligned(x, 2) || !aligned(y, y_type == MOE_WTYPE_F32 ? 4 : 2))
+    return set_error(MOE_EINVAL, "block must be 16-byte aligned, x and y to their elements");
+  size_t off[3], bytes;
+  moe::q4_layout(desc->rows, desc->cols, desc->group, desc->has_zero != 0, off, &bytes);
+  const uint8_t* b = static_cast<const uint8_t*>(block);
+  moe::Q4Linear a = {};
+  a.codes = b + off[0]; a.scales = b + off[1]; a.zeros = desc->has_zero ? b + off[2] : nullptr;
+  a.x = static_cast<const uint16_t*>(x); a.x_ld = x_ld; a.T = T; a.N = desc->rows;
+  a.K = desc->cols; a.y = y; a.y_ld = y_ld; a.y_bf16 = y_type == MOE_WTYPE_BF16;
+  return hip_status(moe::launch_q4_linear(a, desc->group, as_stream(stream)), "moe_q4_linear");
 }
 
 }  // extern "C"

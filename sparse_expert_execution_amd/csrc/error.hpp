@@ -11,4 +11,9 @@ int set_error(int status, const char* fmt, ...) __attribute__((format(printf, 2,
 // descriptor checks and the expert block layout (host.cpp)
 int check_desc(const moe_desc* d);
 void layout(const moe_desc* d, size_t off[6], size_t* bytes);
+// 4-bit integer matrices: columns per scale of an expert weight type (0: not
+// one of them), descriptor checks, sections (codes, scales, zero points)
+int q4_group(int wtype);
+int check_q4(const moe_q4_desc* d);
+void q4_layout(int64_t rows, int64_t cols, int group, bool zero, size_t off[3], size_t* bytes);
 }  // namespace moe

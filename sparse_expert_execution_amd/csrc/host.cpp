@@ -39,7 +39,8 @@ int check_desc(const moe_desc* d) {
     return set_error(MOE_EINVAL, "n_experts %d outside [1, 1024]", d->n_experts);
   if (d->top_k < 1 || d->top_k > d->n_experts || d->top_k > 64)
     return set_error(MOE_EINVAL, "top_k %d outside [1, min(E, 64)]", d->top_k);
-  if (d->wtype != MOE_WTYPE_BF16 && d->wtype != MOE_WTYPE_MXFP4 && d->wtype != MOE_WTYPE_NVFP4)
+  if (d->wtype != MOE_WTYPE_BF16 && d->wtype != MOE_WTYPE_MXFP4 && d->wtype != MOE_WTYPE_NVFP4 &&
+      !q4_group(d->wtype))
     return set_error(MOE_EUNSUPPORTED, "expert weight type %d not supported", d->wtype);
   if (d->router_wtype != MOE_WTYPE_BF16 && d->router_wtype != MOE_WTYPE_F32)
     return set_error(MOE_EUNSUPPORTED, "router weight type %d not supported", d->router_wtype);
@@ -48,8 +49,48 @@ int check_desc(const moe_desc* d) {
   return MOE_OK;
 }
 
+int q4_group(int wtype) {
+  return wtype == MOE_WTYPE_INT4_G32 ? 32 : wtype == MOE_WTYPE_INT4_G64 ? 64
+         : wtype == MOE_WTYPE_INT4_G128 ? 128 : 0;
+}
+
+int check_q4(const moe_q4_desc* d) {
+  if (!d) return set_error(MOE_EINVAL, "q4 desc is null");
+  if (d->rows < 1 || d->cols < 1 || d->rows > 1 << 24 || d->cols > 1 << 20)
+    return set_error(MOE_EINVAL, "q4 rows %d outside [1, 2^24] or cols %d outside [1, 2^20]",
+                     d->rows, d->cols);
+  if ((int64_t)d->rows * d->cols > (int64_t)1 << 36)
+    return set_error(MOE_EINVAL, "q4 matrix of more than 2^36 elements");
+  if (d->group != 32 && d->group != 64 && d->group != 128)
+    return set_error(MOE_EUNSUPPORTED, "q4 group %d is not 32, 64 or 128", d->group);
+  if (d->has_zero != 0 && d->has_zero != 1)
+    return set_error(MOE_EINVAL, "has_zero must be 0 or 1");
+  return MOE_OK;
+}
+
+void q4_layout(int64_t rows, int64_t cols, int group, bool zero, size_t off[3], size_t* bytes) {
+  const size_t tiles = (size_t)((rows + 15) / 16), kb = (size_t)((cols + 127) / 128);
+  const size_t groups = kb * (128 / group);
+  off[0] = 0;
+  off[1] = tiles * kb * 1024;
+  off[2] = off[1] + tiles * groups * 32;
+  *bytes = off[2] + (zero ? tiles * groups * 16 : 0);
+}
+
 void layout(const moe_desc* d, size_t off[6], size_t* bytes) {
   const size_t H = d->hidden, I = d->inter;
+  if (const int g = q4_group(d->wtype)) {
+    size_t at = 0;
+    for (int m = 0; m < 3; ++m) {
+      size_t o[3], n;
+      q4_layout(m < 2 ? d->inter : d->hidden, m < 2 ? d->hidden : d->inter, g, false, o, &n);
+      off[2 * m] = at;
+      off[2 * m + 1] = at + o[1];
+      at += n;
+    }
+    *bytes = align256(at);
+    return;
+  }
   if (d->wtype == MOE_WTYPE_BF16) {
     off[0] = 0;
     off[1] = I * H * 2;
@@ -80,6 +121,15 @@ int moe_expert_layout(const moe_desc* desc, size_t offsets[6], size_t* bytes) {
   if (st) return st;
   if (!offsets || !bytes) return moe::set_error(MOE_EINVAL, "null output pointer");
   moe::layout(desc, offsets, bytes);
+  return MOE_OK;
+}
+
+int moe_q4_layout(const moe_q4_desc* desc, size_t offsets[3], size_t* bytes) {
+  int st = moe::check_q4(desc);
+  if (st) return st;
+  if (!offsets || !bytes) return moe::set_error(MOE_EINVAL, "null output pointer");
+  moe::q4_layout(desc->rows, desc->cols, desc->group, desc->has_zero != 0, offsets, bytes);
+  if (!desc->has_zero) offsets[2] = 0;
   return MOE_OK;
 }
 

@@ -81,6 +81,98 @@ hipError_t launch_route_large(const void* x, const void* w_router, int router_f3
                               int H, int E, int k, int renorm, float* logits, int32_t* ids,
                               float* w, hipStream_t st);
 
+// logits alone, the first launch of launch_route_large
+hipError_t launch_logits(const void* x, const void* w_router, int router_f32, int T, int H, int E,
+                         float* logits, hipStream_t st);
+
+// the gate on given logits, its statistics and its gradient (gate.hip)
+struct GateArgs {
+  const float* z;          // [T][E]
+  const uint8_t* mask;     // [T], zero: not routed; null: all tokens are
+  int T, E, k, renorm;
+  int32_t* ids;            // [T][k]
+  float* w;                // [T][k]
+  int32_t* counts;         // [E + 1] or null
+  float* loss;             // or null
+  // workspace: a row of partial sums per workgroup
+  float* part_s;           // [gate_parts(T)][E]
+  int32_t* part_c;         // [gate_parts(T)][E]
+  int32_t* part_n;         // [gate_parts(T)]
+  float* share;            // [16]
+  unsigned* ticket;
+};
+// workgroups (and rows of partial sums) of the gate: 4 tokens each until 256
+inline int gate_parts(int T) { return T < 1024 ? (T + 3) / 4 : 256; }
+hipError_t launch_gate(const GateArgs& a, hipStream_t st);
+
+struct GateBackward {
+  const float* z;
+  const int32_t* ids;
+  const float* w;
+  const float* dw;         // [T][k] or null
+  const int32_t* counts;   // [E + 1], with dloss
+  const float* dloss;      // one value, or null
+  int T, E, k, renorm;
+  float* dz;               // [T][E]
+};
+hipError_t launch_gate_backward(const GateBackward& a, hipStream_t st);
+
+// gradients of the router's product (router_train.hip)
+struct RouterBackward {
+  const void* x;           // BF16 [T][H]
+  const void* w;           // [E][H]
+  const float* dz;         // [T][E]
+  int router_f32, T, H, E;
+  uint16_t* dx;            // BF16 [T][H] or null
+  float* dw;               // [E][H] or null
+  uint8_t* ws;             // router_backward_bytes
+};
+size_t router_backward_bytes(int T, int H, int E);
+hipError_t launch_router_backward(const RouterBackward& a, hipStream_t st);
+
+// 4-bit integer matrices (q4.hip; layout in q4.hpp)
+struct Q4Linear {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  const uint8_t* zeros;    // null: zero point 8
+  const uint16_t* x;       // BF16, rows x_ld apart
+  int64_t x_ld;
+  int T, N, K;
+  void* y;                 // rows y_ld apart
+  int64_t y_ld;
+  int y_bf16;
+  int tiles, nkb, log_ks;  // set by the launcher
+};
+hipError_t launch_q4_linear(Q4Linear a, int group, hipStream_t st);
+hipError_t launch_q4_quantize(const void* src, int src_bf16, int N, int K, int64_t ld, int group,
+                              uint8_t* codes, uint8_t* scales, uint8_t* zeros, hipStream_t st);
+hipError_t launch_q4_pack(const uint8_t* q, const uint16_t* s, const uint8_t* z, int N, int K,
+                          int group, uint8_t* codes, uint8_t* scales, uint8_t* zeros,
+                          hipStream_t st);
+
+// decode of experts in that format (q4_experts.hip)
+constexpr int kQ4MaxTokens = 64, kQ4MaxPairs = 512;
+constexpr int kQ4MaxItems = kQ4MaxPairs + 8;   // units of up to 16 entries, the shared expert's too
+struct Q4Experts {
+  const uint16_t* x;       // BF16 [T][H]
+  const int32_t* ids;
+  const float* w;
+  const int32_t* slot_of;
+  const uint8_t* pool;
+  const uint8_t* shared;   // or null
+  int64_t expert_bytes;
+  int64_t off[6];
+  int T, H, I, E, k;
+  float* y;                // [T][H]
+  // workspace
+  int2* units;             // [P + 1] entries and slot of the expert whose first pair this is
+  int16_t* lists;          // [P][P] its pairs
+  uint16_t* h_hi;          // [P + T][I] h as two BF16 parts
+  uint16_t* h_lo;
+  int P, log_ks_gu;        // set by the launcher
+};
+hipError_t launch_q4_experts(Q4Experts a, int group, hipStream_t st);
+
 // per-workgroup phase stamps at the end of the decode workspace
 constexpr size_t kDecodeStampBytes = 1024 * 16 * 8;
 // copies of the decode logits (each read by every kZCopies-th workgroup)

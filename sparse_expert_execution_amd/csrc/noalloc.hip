@@ -79,6 +79,9 @@ extern "C" int moe_route_decode_noalloc(const moe_desc* desc, const void* x,
   if (T == 0) return moe_workspace_bytes(desc, 1, MOE_MODE_DECODE) ? MOE_OK : MOE_EINVAL;
   const size_t need = moe_workspace_bytes(desc, T, MOE_MODE_DECODE);
   if (need == 0) return MOE_EINVAL;   // bad descriptor or T: the text is set
+  if (moe::q4_group(desc->wtype))     // its workspace holds no tagged words: it may not share
+    return moe::set_error(MOE_EUNSUPPORTED,
+                          "moe_route_decode_noalloc: 4-bit integer experts take a workspace");
   if (need > moe::kScratchBytes)
     return moe::set_error(MOE_EWORKSPACE,
                           "moe_route_decode_noalloc: T=%d with E=%d, k=%d, I=%d needs %zu bytes "

@@ -1,0 +1,295 @@
+// q4.hip - matrices of 4-bit integers with a scale per group of columns: the
+// dense product y = x W^T, the quantiser and the packer (layout: q4.hpp).
+#include "q4.hpp"
+
+namespace moe {
+namespace {
+
+using namespace q4;
+
+constexpr int kWaves = 8;
+
+// One workgroup: 8 waves as (8 / KS) sets of RT row tiles x KS slices of the
+// columns; a wave walks its slice's column blocks with the next block's loads
+// in flight, and the KS partial sums of a tile meet in LDS, added in slice
+// order.  x goes straight into the matrix operand's registers: lane (n, q)
+// reads 16 bytes of token n, tokens past T read nothing (one token costs four
+// lanes' loads, not 64).
+template <int NT, int RT, int G, bool ZERO, bool VEC>
+__global__ __launch_bounds__(kWaves * 64) void q4_linear_kernel(Q4Linear a) {
+  extern __shared__ v4f red[];                        // [wave][RT * NT][64]
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int n = lane & 15, q = lane >> 4;
+  const int KS = 1 << a.log_ks, slice = wave & (KS - 1), set = wave >> a.log_ks;
+  const int rt0 = (blockIdx.x * (kWaves >> a.log_ks) + set) * RT;
+  const int t0 = blockIdx.y * 16 * NT;
+  const Matrix m{a.codes, a.scales, a.zeros, a.nkb};
+
+  v4f acc[RT][NT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[r][j] = v4f{0.f, 0.f, 0.f, 0.f};
+
+  int tile[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) tile[r] = rt0 + r < a.tiles ? rt0 + r : a.tiles - 1;
+
+  auto load_x = [&](u32x4 (&x)[NT][4], int kb) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int t = t0 + 16 * j + n;
+      const uint16_t* row = a.x + (int64_t)t * a.x_ld;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const int k = 128 * kb + 32 * s + 8 * q;
+        x[j][s] = u32x4{0, 0, 0, 0};
+        if (VEC) {
+          if (t < a.T && k < a.K) x[j][s] = *reinterpret_cast<const u32x4*>(row + k);
+        } else if (t < a.T) {
+          uint32_t v[4] = {0, 0, 0, 0};
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (k + i < a.K) v[i / 2] |= (uint32_t)row[k + i] << (16 * (i % 2));
+          x[j][s] = u32x4{v[0], v[1], v[2], v[3]};
+        }
+      }
+    }
+  };
+
+  Tile<G, ZERO> tl[RT];
+  u32x4 xr[NT][4];
+  if (slice < a.nkb) {
+#pragma unroll
+    for (int r = 0; r < RT; ++r) load_tile<G, ZERO>(tl[r], m, tile[r], slice);
+    load_x(xr, slice);
+  }
+  for (int kb = slice; kb < a.nkb; kb += KS) {
+    Tile<G, ZERO> nt[RT];
+    u32x4 nx[NT][4];
+    const int kn = kb + KS;
+    if (kn < a.nkb) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r) load_tile<G, ZERO>(nt[r], m, tile[r], kn);
+      load_x(nx, kn);
+    }
+    bf16x8 x[NT][1][4];
+    v4f c[NT][128 / G];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) x[j][0][s] = frag(xr[j][s]);
+      if (!ZERO) group_sums<G, 1>(c[j], x[j]);
+    }
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      bf16x8 w[4];
+      tile_weights<G, ZERO>(w, tl[r]);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) mul_tile<G, ZERO, 1>(acc[r][j], tl[r], w, x[j], c[j]);
+    }
+#pragma unroll
+    for (int r = 0; r < RT; ++r) tl[r] = nt[r];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int s = 0; s < 4; ++s) xr[j][s] = nx[j][s];
+  }
+
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) red[(wave * RT * NT + r * NT + j) * 64 + lane] = acc[r][j];
+  __syncthreads();
+  const int items = (kWaves >> a.log_ks) * RT * NT * 64;
+  for (int i = threadIdx.x; i < items; i += kWaves * 64) {
+    const int l = i & 63, f = i >> 6;                 // f: (set, row tile, token tile)
+    const int st = f / (RT * NT), rj = f % (RT * NT);
+    v4f v = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < KS; ++s) v += red[(((st << a.log_ks) + s) * RT * NT + rj) * 64 + l];
+    const int t = t0 + 16 * (rj % NT) + (l & 15);
+    const int row = 16 * ((blockIdx.x * (kWaves >> a.log_ks) + st) * RT + rj / NT) + 4 * (l >> 4);
+    if (t >= a.T || row >= a.N) continue;
+    if (a.y_bf16) {
+      uint16_t* y = static_cast<uint16_t*>(a.y) + (int64_t)t * a.y_ld + row;
+      for (int e = 0; e < 4; ++e)
+        if (row + e < a.N) y[e] = __builtin_bit_cast(uint16_t, (__bf16)v[e]);
+    } else {
+      float* y = static_cast<float*>(a.y) + (int64_t)t * a.y_ld + row;
+      for (int e = 0; e < 4; ++e)
+        if (row + e < a.N) y[e] = v[e];
+    }
+  }
+}
+
+// ---- quantise / pack --------------------------------------------------------
+__device__ __forceinline__ float src_value(const void* src, int bf16, int64_t i) {
+  return bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(src)[i] << 16)
+              : static_cast<const float*>(src)[i];
+}
+
+// One thread per (padded row, group): the group's scale and zero point.
+// Symmetric: s = max|v| / 7, z = 8.  With zero points: the range [min(v, 0),
+// max(v, 0)] in 15 steps.  s is rounded to BF16 before codes are computed from it.
+__global__ __launch_bounds__(256) void q4_scale_kernel(const void* src, int bf16, int N, int K,
+                                                       int64_t ld, int G, int Np, int groups,
+                                                       uint16_t* scales, uint8_t* zeros) {
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (id >= (int64_t)Np * groups) return;
+  const int row = (int)(id / groups), g = (int)(id % groups);
+  float lo = 0.f, hi = 0.f;
+  if (row < N)
+    for (int k = g * G; k < (g + 1) * G && k < K; ++k) {
+      const float v = src_value(src, bf16, (int64_t)row * ld + k);
+      lo = fminf(lo, v);
+      hi = fmaxf(hi, v);
+    }
+  const float s = zeros ? (hi - lo) / 15.f : fmaxf(hi, -lo) / 7.f;
+  const __bf16 sb = (__bf16)s;
+  const float sr = (float)sb;
+  const int64_t at = ((int64_t)(row / 16) * groups + g) * 16 + row % 16;
+  scales[at] = __builtin_bit_cast(uint16_t, sb);
+  if (zeros) zeros[at] = sr > 0.f ? (uint8_t)fminf(fmaxf(rintf(-lo / sr), 0.f), 15.f) : 8;
+}
+
+// One thread per (tile, lane): its 32 codes.
+__global__ __launch_bounds__(256) void q4_code_kernel(const void* src, int bf16, int N, int K,
+                                                      int64_t ld, int G, int nkb, int64_t lanes,
+                                                      const uint16_t* scales,
+                                                      const uint8_t* zeros, uint4* codes) {
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (id >= lanes) return;
+  const int lane = (int)(id & 63);
+  const int64_t at = id >> 6;
+  const int kb = (int)(at % nkb), row = (int)(at / nkb) * 16 + (lane & 15);
+  uint32_t out[4];
+  for (int s = 0; s < 4; ++s) {
+    uint32_t w = 0;
+    for (int i = 0; i < 8; ++i) {
+      const int k = 128 * kb + 32 * s + 8 * (lane >> 4) + i;
+      const int64_t gi = ((int64_t)(row / 16) * (nkb * (128 / G)) + k / G) * 16 + row % 16;
+      const float sc = __uint_as_float((uint32_t)scales[gi] << 16);
+      const float z = zeros ? (float)zeros[gi] : 8.f;
+      float q = z;
+      if (row < N && k < K && sc > 0.f)
+        q = fminf(fmaxf(rintf(src_value(src, bf16, (int64_t)row * ld + k) / sc) + z, 0.f), 15.f);
+      w |= ((uint32_t)q & 15u) << (4 * (i / 2 + 4 * (i % 2)));
+    }
+    out[s] = w;
+  }
+  codes[id] = make_uint4(out[0], out[1], out[2], out[3]);
+}
+
+// One thread per (tile, lane): codes given row-major [N][ceil(K / 2)], low
+// nibble first.
+__global__ __launch_bounds__(256) void q4_pack_codes_kernel(const uint8_t* src, int N, int K,
+                                                            int nkb, int64_t lanes,
+                                                            uint4* codes) {
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (id >= lanes) return;
+  const int lane = (int)(id & 63);
+  const int64_t at = id >> 6;
+  const int kb = (int)(at % nkb), row = (int)(at / nkb) * 16 + (lane & 15);
+  uint32_t out[4];
+  for (int s = 0; s < 4; ++s) {
+    uint32_t w = 0;
+    for (int i = 0; i < 8; ++i) {
+      const int k = 128 * kb + 32 * s + 8 * (lane >> 4) + i;
+      uint32_t q = 8;
+      if (row < N && k < K) q = src[(int64_t)row * ((K + 1) / 2) + k / 2] >> (4 * (k % 2)) & 15u;
+      w |= q << (4 * (i / 2 + 4 * (i % 2)));
+    }
+    out[s] = w;
+  }
+  codes[id] = make_uint4(out[0], out[1], out[2], out[3]);
+}
+
+__global__ __launch_bounds__(256) void q4_pack_scales_kernel(const uint16_t* s, const uint8_t* z,
+                                                             int N, int given, int Np, int groups,
+                                                             uint16_t* scales, uint8_t* zeros) {
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (id >= (int64_t)Np * groups) return;
+  const int row = (int)(id / groups), g = (int)(id % groups);
+  const bool in = row < N && g < given;
+  const int64_t at = ((int64_t)(row / 16) * groups + g) * 16 + row % 16;
+  scales[at] = in ? s[(int64_t)row * given + g] : 0;
+  if (zeros) zeros[at] = in ? z[(int64_t)row * given + g] : 8;
+}
+
+template <int NT, int RT, int G, bool ZERO>
+hipError_t run_linear(const Q4Linear& a, dim3 grid, bool vec, hipStream_t st) {
+  const size_t lds = (size_t)kWaves * RT * NT * 64 * sizeof(v4f);
+  if (vec)
+    hipLaunchKernelGGL((q4_linear_kernel<NT, RT, G, ZERO, true>), grid, dim3(kWaves * 64), lds,
+                       st, a);
+  else
+    hipLaunchKernelGGL((q4_linear_kernel<NT, RT, G, ZERO, false>), grid, dim3(kWaves * 64), lds,
+                       st, a);
+  return hipGetLastError();
+}
+
+template <int NT, int RT>
+hipError_t pick_linear(const Q4Linear& a, int G, dim3 grid, bool vec, hipStream_t st) {
+  if (a.zeros) {
+    if (G == 32) return run_linear<NT, RT, 32, true>(a, grid, vec, st);
+    if (G == 64) return run_linear<NT, RT, 64, true>(a, grid, vec, st);
+    return run_linear<NT, RT, 128, true>(a, grid, vec, st);
+  }
+  if (G == 32) return run_linear<NT, RT, 32, false>(a, grid, vec, st);
+  if (G == 64) return run_linear<NT, RT, 64, false>(a, grid, vec, st);
+  return run_linear<NT, RT, 128, false>(a, grid, vec, st);
+}
+
+}  // namespace
+
+hipError_t launch_q4_linear(Q4Linear a, int group, hipStream_t st) {
+  a.tiles = (a.N + 15) / 16;
+  a.nkb = (a.K + 127) / 128;
+  a.log_ks = a.nkb >= 8 ? 3 : a.nkb >= 4 ? 2 : a.nkb >= 2 ? 1 : 0;
+  const bool vec = a.K % 8 == 0 && a.x_ld % 8 == 0 && (reinterpret_cast<uintptr_t>(a.x) & 15) == 0;
+  const int sets = kWaves >> a.log_ks;
+  const int nt = a.T <= 16 ? 1 : a.T <= 32 ? 2 : 4;
+  const int rt = a.tiles >= 2048 ? 2 : 1;
+  const dim3 grid((a.tiles + sets * rt - 1) / (sets * rt), (a.T + 16 * nt - 1) / (16 * nt));
+  if (rt == 2) {
+    if (nt == 1) return pick_linear<1, 2>(a, group, grid, vec, st);
+    if (nt == 2) return pick_linear<2, 2>(a, group, grid, vec, st);
+    return pick_linear<4, 2>(a, group, grid, vec, st);
+  }
+  if (nt == 1) return pick_linear<1, 1>(a, group, grid, vec, st);
+  if (nt == 2) return pick_linear<2, 1>(a, group, grid, vec, st);
+  return pick_linear<4, 1>(a, group, grid, vec, st);
+}
+
+hipError_t launch_q4_quantize(const void* src, int bf16, int N, int K, int64_t ld, int group,
+                              uint8_t* codes, uint8_t* scales, uint8_t* zeros, hipStream_t st) {
+  const int nkb = (K + 127) / 128, tiles = (N + 15) / 16, groups = nkb * (128 / group);
+  const int64_t sg = (int64_t)tiles * 16 * groups, lanes = (int64_t)tiles * nkb * 64;
+  hipLaunchKernelGGL(q4_scale_kernel, dim3((unsigned)((sg + 255) / 256)), dim3(256), 0, st, src,
+                     bf16, N, K, ld, group, tiles * 16, groups,
+                     reinterpret_cast<uint16_t*>(scales), zeros);
+  hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return err;
+  hipLaunchKernelGGL(q4_code_kernel, dim3((unsigned)((lanes + 255) / 256)), dim3(256), 0, st, src,
+                     bf16, N, K, ld, group, nkb, lanes,
+                     reinterpret_cast<const uint16_t*>(scales), zeros,
+                     reinterpret_cast<uint4*>(codes));
+  return hipGetLastError();
+}
+
+hipError_t launch_q4_pack(const uint8_t* q, const uint16_t* s, const uint8_t* z, int N, int K,
+                          int group, uint8_t* codes, uint8_t* scales, uint8_t* zeros,
+                          hipStream_t st) {
+  const int nkb = (K + 127) / 128, tiles = (N + 15) / 16, groups = nkb * (128 / group);
+  const int64_t sg = (int64_t)tiles * 16 * groups, lanes = (int64_t)tiles * nkb * 64;
+  hipLaunchKernelGGL(q4_pack_scales_kernel, dim3((unsigned)((sg + 255) / 256)), dim3(256), 0, st,
+                     s, z, N, (K + group - 1) / group, tiles * 16, groups,
+                     reinterpret_cast<uint16_t*>(scales), zeros);
+  hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return err;
+  hipLaunchKernelGGL(q4_pack_codes_kernel, dim3((unsigned)((lanes + 255) / 256)), dim3(256), 0,
+                     st, q, N, K, nkb, lanes, reinterpret_cast<uint4*>(codes));
+  return hipGetLastError();
+}
+
+}  // namespace moe

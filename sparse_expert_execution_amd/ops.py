@@ -9,7 +9,8 @@ import ctypes
 import torch
 
 from . import _lib
-from ._lib import MoeDesc, MoePlan, check, lib
+from ._lib import (MODE_DECODE, MODE_GATE, MODE_PREFILL, MODE_ROUTE,  # noqa: F401
+                   MODE_ROUTER_BACKWARD, MoeDesc, MoePlan, MoeQ4Desc, check, lib)
 
 
 def _ptr(t):
@@ -23,7 +24,9 @@ def _stream(stream=None):
 
 def make_desc(hidden, inter, n_experts, top_k, has_shared=False, renorm=False,
               wtype="mxfp4", router_wtype="bf16"):
-    wt = {"bf16": _lib.WTYPE_BF16, "mxfp4": _lib.WTYPE_MXFP4, "nvfp4": _lib.WTYPE_NVFP4}[wtype]
+    wt = {"bf16": _lib.WTYPE_BF16, "mxfp4": _lib.WTYPE_MXFP4, "nvfp4": _lib.WTYPE_NVFP4,
+          "int4_g32": _lib.WTYPE_INT4_G32, "int4_g64": _lib.WTYPE_INT4_G64,
+          "int4_g128": _lib.WTYPE_INT4_G128}[wtype]
     rt = {"f32": _lib.WTYPE_F32, "bf16": _lib.WTYPE_BF16}[router_wtype]
     return MoeDesc(hidden, inter, n_experts, top_k, int(has_shared), int(renorm), wt, rt)
 
@@ -50,6 +53,103 @@ def route(desc, x, w_router, ids, w, ws, stream=None):
     T = x.shape[0]
     check(lib().moe_route(ctypes.byref(desc), _ptr(x), _ptr(w_router), T, _ptr(ids),
                           _ptr(w), _ptr(ws), ws.numel(), _stream(stream)), "moe_route")
+
+
+def _take(name, t, dtype, shape, device=None, rows=False):
+    """Checks one tensor argument: type, shape, contiguity (rows: only the last
+    axis need be), and the device it shares with the others.  Returns its device."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if rows:
+        if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or \
+                (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+            raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    elif not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, which is not the current device")
+    return t.device
+
+
+def _take_ws(ws, device):
+    _take("ws", ws, torch.uint8, (ws.numel(),), device)
+    return _ptr(ws), ws.numel()
+
+
+def router_logits(desc, x, w_router, logits, stream=None):
+    """moe_router_logits: x [T, H] bf16, w_router [E, H] -> logits [T, E] float32."""
+    T = x.shape[0]
+    dev = _take("x", x, torch.bfloat16, (T, desc.hidden))
+    _take("w_router", w_router, _router_type(desc), (desc.n_experts, desc.hidden), dev)
+    _take("logits", logits, torch.float32, (T, desc.n_experts), dev)
+    check(lib().moe_router_logits(ctypes.byref(desc), _ptr(x), _ptr(w_router), T, _ptr(logits),
+                                  _stream(stream)), "moe_router_logits")
+
+
+def _router_type(desc):
+    return torch.float32 if desc.router_wtype == _lib.WTYPE_F32 else torch.bfloat16
+
+
+def gate(desc, logits, ids, w, ws=None, mask=None, counts=None, loss=None, stream=None):
+    """moe_gate: logits [T, E] float32 -> ids [T, k] int32, w [T, k] float32 and,
+    where given, counts [E + 1] int32 (the last: routed tokens) and loss [1]
+    float32.  mask: [T] uint8 or bool, zero where a token is padding.  ws (of
+    MODE_GATE) is needed with counts or loss."""
+    T, E, k = logits.shape[0], desc.n_experts, desc.top_k
+    dev = _take("logits", logits, torch.float32, (T, E))
+    _take("ids", ids, torch.int32, (T, k), dev)
+    _take("w", w, torch.float32, (T, k), dev)
+    if mask is not None:
+        _take("mask", mask, torch.bool if mask.dtype == torch.bool else torch.uint8, (T,), dev)
+    if counts is not None:
+        _take("counts", counts, torch.int32, (E + 1,), dev)
+    if loss is not None:
+        _take("loss", loss, torch.float32, (1,), dev)
+    wsp, wsn = (None, 0) if ws is None else _take_ws(ws, dev)
+    check(lib().moe_gate(ctypes.byref(desc), _ptr(logits), T, _ptr(mask), _ptr(ids), _ptr(w),
+                         _ptr(counts), _ptr(loss), wsp, wsn, _stream(stream)), "moe_gate")
+
+
+def gate_backward(desc, logits, ids, w, dlogits, dw=None, counts=None, dloss=None, stream=None):
+    """moe_gate_backward: the gradient of (dw * w).sum() + dloss * loss into the
+    logits, from what gate took and gave.  dw [T, k] float32, dloss [1] float32
+    on the device (with counts); either may be None.  dlogits [T, E] float32 is
+    overwritten."""
+    T, E, k = logits.shape[0], desc.n_experts, desc.top_k
+    dev = _take("logits", logits, torch.float32, (T, E))
+    _take("ids", ids, torch.int32, (T, k), dev)
+    for name, t, dt, shape in (("w", w, torch.float32, (T, k)), ("dw", dw, torch.float32, (T, k)),
+                               ("counts", counts, torch.int32, (E + 1,)),
+                               ("dloss", dloss, torch.float32, (1,))):
+        if t is not None:
+            _take(name, t, dt, shape, dev)
+    _take("dlogits", dlogits, torch.float32, (T, E), dev)
+    check(lib().moe_gate_backward(ctypes.byref(desc), _ptr(logits), T, _ptr(ids), _ptr(w),
+                                  _ptr(dw), _ptr(counts), _ptr(dloss), _ptr(dlogits),
+                                  _stream(stream)), "moe_gate_backward")
+
+
+def router_backward(desc, x, w_router, dlogits, ws, dx=None, dw_router=None, stream=None):
+    """moe_router_backward: dx [T, H] bf16 = dlogits @ w_router and dw_router
+    [E, H] float32 = dlogits.T @ x, each where given.  ws of MODE_ROUTER_BACKWARD."""
+    T, H, E = dlogits.shape[0], desc.hidden, desc.n_experts
+    dev = _take("dlogits", dlogits, torch.float32, (T, E))
+    if x is not None:
+        _take("x", x, torch.bfloat16, (T, H), dev)
+    if w_router is not None:
+        _take("w_router", w_router, _router_type(desc), (E, H), dev)
+    if dx is not None:
+        _take("dx", dx, torch.bfloat16, (T, H), dev)
+    if dw_router is not None:
+        _take("dw_router", dw_router, torch.float32, (E, H), dev)
+    wsp, wsn = _take_ws(ws, dev)
+    check(lib().moe_router_backward(ctypes.byref(desc), _ptr(x), _ptr(w_router), T,
+                                    _ptr(dlogits), _ptr(dx), _ptr(dw_router), wsp, wsn,
+                                    _stream(stream)), "moe_router_backward")
 
 
 def decode(desc, x, ids, w, pool, y, ws, slot_of=None, shared=None, stream=None):
@@ -122,6 +222,67 @@ def quantize_mxfp4(src, codes, scales, stream=None):
     rows, K = src.shape
     check(lib().moe_quantize_mxfp4(_ptr(src), rows, K, src.stride(0), _ptr(codes),
                                    _ptr(scales), _stream(stream)), "moe_quantize_mxfp4")
+
+
+def make_q4(rows, cols, group=128, zero=False):
+    """Descriptor of a matrix of 4-bit integers (moe_q4_desc)."""
+    return MoeQ4Desc(rows, cols, group, int(zero))
+
+
+def q4_layout(desc):
+    """moe_q4_layout: ([codes, scales, zero points] offsets, bytes)."""
+    off = (ctypes.c_size_t * 3)()
+    n = ctypes.c_size_t()
+    check(lib().moe_q4_layout(ctypes.byref(desc), off, ctypes.byref(n)), "moe_q4_layout")
+    return list(off), n.value
+
+
+def _take_block(desc, block, device):
+    need = q4_layout(desc)[1]
+    _take("block", block, torch.uint8, (block.numel(),), device)
+    if block.numel() < need:
+        raise ValueError(f"block has {block.numel()} bytes, the matrix takes {need}")
+
+
+def q4_quantize(desc, src, block, stream=None):
+    """moe_q4_quantize: src [rows, cols] float32 or bf16 (device, contiguous
+    rows) -> block, a uint8 device tensor of q4_layout's bytes."""
+    if src.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("src must be float32 or bfloat16")
+    dev = _take("src", src, src.dtype, (desc.rows, desc.cols), rows=True)
+    _take_block(desc, block, dev)
+    check(lib().moe_q4_quantize(ctypes.byref(desc), _ptr(src),
+                                _lib.WTYPE_F32 if src.dtype == torch.float32 else _lib.WTYPE_BF16,
+                                max(src.stride(0), desc.cols), _ptr(block), _stream(stream)),
+          "moe_q4_quantize")
+
+
+def q4_pack(desc, codes, scales, block, zeros=None, stream=None):
+    """moe_q4_pack: codes [rows, ceil(cols / 2)] uint8, scales [rows,
+    ceil(cols / group)] bf16, zeros uint8 of that shape (with zero=True) -> block."""
+    g = -(-desc.cols // desc.group)
+    dev = _take("codes", codes, torch.uint8, (desc.rows, (desc.cols + 1) // 2))
+    _take("scales", scales, torch.bfloat16, (desc.rows, g), dev)
+    if zeros is not None:
+        _take("zeros", zeros, torch.uint8, (desc.rows, g), dev)
+    _take_block(desc, block, dev)
+    check(lib().moe_q4_pack(ctypes.byref(desc), _ptr(codes), _ptr(scales), _ptr(zeros),
+                            _ptr(block), _stream(stream)), "moe_q4_pack")
+
+
+def q4_linear(desc, x, block, y, stream=None):
+    """moe_q4_linear: y [T, rows] = x [T, cols] @ W.T; x bf16, y float32 or bf16,
+    both with contiguous rows (any row stride)."""
+    T = x.shape[0]
+    dev = _take("x", x, torch.bfloat16, (T, desc.cols), rows=True)
+    if y.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("y must be float32 or bfloat16")
+    _take("y", y, y.dtype, (T, desc.rows), dev, rows=True)
+    _take_block(desc, block, dev)
+    check(lib().moe_q4_linear(ctypes.byref(desc), _ptr(x), max(x.stride(0), desc.cols), T,
+                              _ptr(block), _ptr(y),
+                              _lib.WTYPE_F32 if y.dtype == torch.float32 else _lib.WTYPE_BF16,
+                              max(y.stride(0), desc.rows), _stream(stream)), "moe_q4_linear")
 
 
 def dequant_mxfp4(codes, scales, out, stream=None):
