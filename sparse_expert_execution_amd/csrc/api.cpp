@@ -84,20 +84,21 @@ RouteWs route_ws(const moe_desc* d, int T, bool decode) {
 }
 
 // decode workspace of 4-bit integer experts: the header (the router's ticket
-// is its first word), logits z [T][E], the units' (entries, slot) and pair
-// lists, h of every pair and of the shared expert's tokens in two BF16 parts.
+// is its first word), logits z [T][E], the number of units, the units and
+// their entries, h of every pair and of the shared expert's tokens in three
+// BF16 parts.
 struct Q4DecodeWs {
-  size_t z, units, lists, h_hi, h_lo, total;
+  size_t z, n_units, units, entries, h, total;
 };
 Q4DecodeWs q4_decode_ws(const moe_desc* d, int T) {
   Q4DecodeWs w;
-  const size_t P = (size_t)T * d->top_k, h = (P + T) * d->inter * 2;
+  const size_t P = (size_t)T * d->top_k;
   size_t o = kDecodeHeader;
   w.z = o; o = align_up(o + (size_t)T * d->n_experts * 4);
-  w.units = o; o = align_up(o + (P + 1) * 8);
-  w.lists = o; o = align_up(o + P * P * 2);
-  w.h_hi = o; o = align_up(o + h);
-  w.h_lo = o; o = align_up(o + h);
+  w.n_units = o; o = align_up(o + 4);
+  w.units = o; o = align_up(o + (P + 1) * 16);
+  w.entries = o; o = align_up(o + (P + T) * 2);
+  w.h = o; o = align_up(o + 3 * (P + T) * d->inter * 2);
   w.total = o;
   return w;
 }
@@ -227,10 +228,10 @@ static int q4_decode_impl(const moe_desc* desc, const void* x, const void* w_rou
   for (int i = 0; i < 6; ++i) a.off[i] = (int64_t)off[i];
   a.T = T; a.H = desc->hidden; a.I = desc->inter; a.E = desc->n_experts; a.k = desc->top_k;
   a.y = y;
-  a.units = reinterpret_cast<int2*>(b + L.units);
-  a.lists = reinterpret_cast<int16_t*>(b + L.lists);
-  a.h_hi = reinterpret_cast<uint16_t*>(b + L.h_hi);
-  a.h_lo = reinterpret_cast<uint16_t*>(b + L.h_lo);
+  a.n_units = reinterpret_cast<int32_t*>(b + L.n_units);
+  a.units = reinterpret_cast<int4*>(b + L.units);
+  a.entries = reinterpret_cast<int16_t*>(b + L.entries);
+  a.h = reinterpret_cast<uint16_t*>(b + L.h);
   return hip_status(moe::launch_q4_experts(a, moe::q4_group(desc->wtype), as_stream(stream)),
                     name);
 }

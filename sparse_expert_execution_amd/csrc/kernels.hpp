@@ -152,7 +152,6 @@ hipError_t launch_q4_pack(const uint8_t* q, const uint16_t* s, const uint8_t* z,
 
 // decode of experts in that format (q4_experts.hip)
 constexpr int kQ4MaxTokens = 64, kQ4MaxPairs = 512;
-constexpr int kQ4MaxItems = kQ4MaxPairs + 8;   // units of up to 16 entries, the shared expert's too
 struct Q4Experts {
   const uint16_t* x;       // BF16 [T][H]
   const int32_t* ids;
@@ -165,11 +164,11 @@ struct Q4Experts {
   int T, H, I, E, k;
   float* y;                // [T][H]
   // workspace
-  int2* units;             // [P + 1] entries and slot of the expert whose first pair this is
-  int16_t* lists;          // [P][P] its pairs
-  uint16_t* h_hi;          // [P + T][I] h as two BF16 parts
-  uint16_t* h_lo;
-  int P, log_ks_gu;        // set by the launcher
+  int32_t* n_units;
+  int4* units;             // [P + 1] slot (-1: the shared expert), first entry, entries, 0
+  int16_t* entries;        // [P + T] pair numbers, P + t for the shared expert
+  uint16_t* h;             // [3][P + T][I] h as three BF16 parts
+  int P;                   // set by the launcher
 };
 hipError_t launch_q4_experts(Q4Experts a, int group, hipStream_t st);
 

@@ -10,115 +10,97 @@ using namespace q4;
 constexpr int kWaves = 8;
 
 // One workgroup: 8 waves as (8 / KS) sets of RT row tiles x KS slices of the
-// columns; a wave walks its slice's column blocks with the next block's loads
-// in flight, and the KS partial sums of a tile meet in LDS, added in slice
-// order.  x goes straight into the matrix operand's registers: lane (n, q)
-// reads 16 bytes of token n, tokens past T read nothing (one token costs four
-// lanes' loads, not 64).
-template <int NT, int RT, int G, bool ZERO, bool VEC>
-__global__ __launch_bounds__(kWaves * 64) void q4_linear_kernel(Q4Linear a) {
-  extern __shared__ v4f red[];                        // [wave][RT * NT][64]
+// columns; a wave walks its slice's column blocks with D - 1 blocks' loads in
+// flight, and the KS partial sums of a tile meet in LDS, added in slice order.
+// x goes straight into the matrix operand's registers: lane (r, q) reads 16
+// bytes of the token in slot r, empty slots read nothing (one token costs
+// four lanes' loads, not 64).
+template <int NT, int TI, int RT, int G, bool ZERO, bool VEC>
+__global__ __launch_bounds__(kWaves * 64, NT == 4 ? 2 : NT == 2 ? 3 : 4) void
+q4_linear_kernel(Q4Linear a) {
+  constexpr int D = NT == 1 && RT == 1 ? 3 : NT == 4 && G == 32 ? 1 : 2;
+  extern __shared__ float red[];                      // [wave][RT * NT][TI][64]
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int n = lane & 15, q = lane >> 4;
+  const int q = lane >> 4;
   const int KS = 1 << a.log_ks, slice = wave & (KS - 1), set = wave >> a.log_ks;
   const int rt0 = (blockIdx.x * (kWaves >> a.log_ks) + set) * RT;
   const int t0 = blockIdx.y * 16 * NT;
   const Matrix m{a.codes, a.scales, a.zeros, a.nkb};
 
-  v4f acc[RT][NT];
+  float acc[RT][NT][TI];
 #pragma unroll
   for (int r = 0; r < RT; ++r)
 #pragma unroll
-    for (int j = 0; j < NT; ++j) acc[r][j] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int i = 0; i < TI; ++i) acc[r][j][i] = 0.f;
 
   int tile[RT];
 #pragma unroll
   for (int r = 0; r < RT; ++r) tile[r] = rt0 + r < a.tiles ? rt0 + r : a.tiles - 1;
 
-  auto load_x = [&](u32x4 (&x)[NT][4], int kb) {
+  struct Block {
+    Tile<G, ZERO> t[RT];
+    bf16x8 x[NT][4];
+  };
+  auto load = [&](Block& b, int it) {
+    const int last = (a.nkb - 1 - slice) >> a.log_ks;   // >= 0: KS <= nkb
+    const int kb = slice + ((it < last ? it : last) << a.log_ks);
+#pragma unroll
+    for (int r = 0; r < RT; ++r) load_tile<G, ZERO>(b.t[r], m, tile[r], kb);
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      const int t = t0 + 16 * j + n;
+      const int t = t0 + 16 * j + slot_token(lane & 15);
       const uint16_t* row = a.x + (int64_t)t * a.x_ld;
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
         const int k = 128 * kb + 32 * s + 8 * q;
-        x[j][s] = u32x4{0, 0, 0, 0};
+        u32x4 v = u32x4{0, 0, 0, 0};
         if (VEC) {
-          if (t < a.T && k < a.K) x[j][s] = *reinterpret_cast<const u32x4*>(row + k);
+          if (t < a.T && k < a.K) v = *reinterpret_cast<const u32x4*>(row + k);
         } else if (t < a.T) {
-          uint32_t v[4] = {0, 0, 0, 0};
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             if (k + i < a.K) v[i / 2] |= (uint32_t)row[k + i] << (16 * (i % 2));
-          x[j][s] = u32x4{v[0], v[1], v[2], v[3]};
         }
+        b.x[j][s] = frag(v);
       }
     }
   };
 
-  Tile<G, ZERO> tl[RT];
-  u32x4 xr[NT][4];
-  if (slice < a.nkb) {
+  const int n_it = (a.nkb - slice + KS - 1) >> a.log_ks;
+  Block b[D];
 #pragma unroll
-    for (int r = 0; r < RT; ++r) load_tile<G, ZERO>(tl[r], m, tile[r], slice);
-    load_x(xr, slice);
-  }
-  for (int kb = slice; kb < a.nkb; kb += KS) {
-    Tile<G, ZERO> nt[RT];
-    u32x4 nx[NT][4];
-    const int kn = kb + KS;
-    if (kn < a.nkb) {
+  for (int d = 0; d < D - 1; ++d) load(b[d], d);
+  for (int i0 = 0; i0 < n_it; i0 += D) {
 #pragma unroll
-      for (int r = 0; r < RT; ++r) load_tile<G, ZERO>(nt[r], m, tile[r], kn);
-      load_x(nx, kn);
+    for (int d = 0; d < D; ++d) {
+      if (i0 + d >= n_it) break;
+      load(b[(d + D - 1) % D], i0 + d + D - 1);       // past the end: the last again
+      mul_tiles<RT, NT, TI, G, ZERO>(acc, b[d].t, b[d].x);
     }
-    bf16x8 x[NT][1][4];
-    v4f c[NT][128 / G];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-#pragma unroll
-      for (int s = 0; s < 4; ++s) x[j][0][s] = frag(xr[j][s]);
-      if (!ZERO) group_sums<G, 1>(c[j], x[j]);
-    }
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      bf16x8 w[4];
-      tile_weights<G, ZERO>(w, tl[r]);
-#pragma unroll
-      for (int j = 0; j < NT; ++j) mul_tile<G, ZERO, 1>(acc[r][j], tl[r], w, x[j], c[j]);
-    }
-#pragma unroll
-    for (int r = 0; r < RT; ++r) tl[r] = nt[r];
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int s = 0; s < 4; ++s) xr[j][s] = nx[j][s];
   }
 
 #pragma unroll
   for (int r = 0; r < RT; ++r)
 #pragma unroll
-    for (int j = 0; j < NT; ++j) red[(wave * RT * NT + r * NT + j) * 64 + lane] = acc[r][j];
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int i = 0; i < TI; ++i)
+        red[((wave * RT * NT + r * NT + j) * TI + i) * 64 + lane] = acc[r][j][i];
   __syncthreads();
-  const int items = (kWaves >> a.log_ks) * RT * NT * 64;
-  for (int i = threadIdx.x; i < items; i += kWaves * 64) {
-    const int l = i & 63, f = i >> 6;                 // f: (set, row tile, token tile)
-    const int st = f / (RT * NT), rj = f % (RT * NT);
-    v4f v = v4f{0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < KS; ++s) v += red[(((st << a.log_ks) + s) * RT * NT + rj) * 64 + l];
-    const int t = t0 + 16 * (rj % NT) + (l & 15);
-    const int row = 16 * ((blockIdx.x * (kWaves >> a.log_ks) + st) * RT + rj / NT) + 4 * (l >> 4);
+  const int items = (kWaves >> a.log_ks) * RT * NT * TI * 64;
+  for (int id = threadIdx.x; id < items; id += kWaves * 64) {
+    const int l = id & 63, f = id >> 6;               // f: (set, row tile, token tile, result)
+    const int st = f / (RT * NT * TI), rji = f % (RT * NT * TI);
+    float v = 0.f;
+    for (int s = 0; s < KS; ++s) v += red[(((st << a.log_ks) + s) * RT * NT * TI + rji) * 64 + l];
+    const int rj = rji / TI, t = t0 + 16 * (rj % NT) + result_token(l, rji % TI);
+    const int row = 16 * ((blockIdx.x * (kWaves >> a.log_ks) + st) * RT + rj / NT) + (l & 15);
     if (t >= a.T || row >= a.N) continue;
-    if (a.y_bf16) {
-      uint16_t* y = static_cast<uint16_t*>(a.y) + (int64_t)t * a.y_ld + row;
-      for (int e = 0; e < 4; ++e)
-        if (row + e < a.N) y[e] = __builtin_bit_cast(uint16_t, (__bf16)v[e]);
-    } else {
-      float* y = static_cast<float*>(a.y) + (int64_t)t * a.y_ld + row;
-      for (int e = 0; e < 4; ++e)
-        if (row + e < a.N) y[e] = v[e];
-    }
+    const int64_t at = (int64_t)t * a.y_ld + row;
+    if (a.y_bf16) static_cast<uint16_t*>(a.y)[at] = __builtin_bit_cast(uint16_t, (__bf16)v);
+    else static_cast<float*>(a.y)[at] = v;
   }
 }
 
@@ -216,28 +198,37 @@ __global__ __launch_bounds__(256) void q4_pack_scales_kernel(const uint16_t* s, 
   if (zeros) zeros[at] = in ? z[(int64_t)row * given + g] : 8;
 }
 
-template <int NT, int RT, int G, bool ZERO>
+template <int NT, int TI, int RT, int G, bool ZERO>
 hipError_t run_linear(const Q4Linear& a, dim3 grid, bool vec, hipStream_t st) {
-  const size_t lds = (size_t)kWaves * RT * NT * 64 * sizeof(v4f);
+  const size_t lds = (size_t)kWaves * RT * NT * TI * 64 * sizeof(float);
   if (vec)
-    hipLaunchKernelGGL((q4_linear_kernel<NT, RT, G, ZERO, true>), grid, dim3(kWaves * 64), lds,
-                       st, a);
+    hipLaunchKernelGGL((q4_linear_kernel<NT, TI, RT, G, ZERO, true>), grid, dim3(kWaves * 64),
+                       lds, st, a);
   else
-    hipLaunchKernelGGL((q4_linear_kernel<NT, RT, G, ZERO, false>), grid, dim3(kWaves * 64), lds,
-                       st, a);
+    hipLaunchKernelGGL((q4_linear_kernel<NT, TI, RT, G, ZERO, false>), grid, dim3(kWaves * 64),
+                       lds, st, a);
   return hipGetLastError();
 }
 
-template <int NT, int RT>
-hipError_t pick_linear(const Q4Linear& a, int G, dim3 grid, bool vec, hipStream_t st) {
+template <int NT, int TI, int RT>
+hipError_t pick_group(const Q4Linear& a, int G, dim3 grid, bool vec, hipStream_t st) {
   if (a.zeros) {
-    if (G == 32) return run_linear<NT, RT, 32, true>(a, grid, vec, st);
-    if (G == 64) return run_linear<NT, RT, 64, true>(a, grid, vec, st);
-    return run_linear<NT, RT, 128, true>(a, grid, vec, st);
+    if (G == 32) return run_linear<NT, TI, RT, 32, true>(a, grid, vec, st);
+    if (G == 64) return run_linear<NT, TI, RT, 64, true>(a, grid, vec, st);
+    return run_linear<NT, TI, RT, 128, true>(a, grid, vec, st);
   }
-  if (G == 32) return run_linear<NT, RT, 32, false>(a, grid, vec, st);
-  if (G == 64) return run_linear<NT, RT, 64, false>(a, grid, vec, st);
-  return run_linear<NT, RT, 128, false>(a, grid, vec, st);
+  if (G == 32) return run_linear<NT, TI, RT, 32, false>(a, grid, vec, st);
+  if (G == 64) return run_linear<NT, TI, RT, 64, false>(a, grid, vec, st);
+  return run_linear<NT, TI, RT, 128, false>(a, grid, vec, st);
+}
+
+template <int RT>
+hipError_t pick_tokens(const Q4Linear& a, int G, dim3 grid, bool vec, hipStream_t st) {
+  if (a.T <= 4) return pick_group<1, 1, RT>(a, G, grid, vec, st);
+  if (a.T <= 8) return pick_group<1, 2, RT>(a, G, grid, vec, st);
+  if (a.T <= 16) return pick_group<1, 4, RT>(a, G, grid, vec, st);
+  if (a.T <= 32) return pick_group<2, 4, 1>(a, G, grid, vec, st);
+  return pick_group<4, 4, 1>(a, G, grid, vec, st);
 }
 
 }  // namespace
@@ -249,16 +240,10 @@ hipError_t launch_q4_linear(Q4Linear a, int group, hipStream_t st) {
   const bool vec = a.K % 8 == 0 && a.x_ld % 8 == 0 && (reinterpret_cast<uintptr_t>(a.x) & 15) == 0;
   const int sets = kWaves >> a.log_ks;
   const int nt = a.T <= 16 ? 1 : a.T <= 32 ? 2 : 4;
-  const int rt = a.tiles >= 2048 ? 2 : 1;
+  const int rt = a.tiles >= 2048 && nt == 1 ? 2 : 1;
   const dim3 grid((a.tiles + sets * rt - 1) / (sets * rt), (a.T + 16 * nt - 1) / (16 * nt));
-  if (rt == 2) {
-    if (nt == 1) return pick_linear<1, 2>(a, group, grid, vec, st);
-    if (nt == 2) return pick_linear<2, 2>(a, group, grid, vec, st);
-    return pick_linear<4, 2>(a, group, grid, vec, st);
-  }
-  if (nt == 1) return pick_linear<1, 1>(a, group, grid, vec, st);
-  if (nt == 2) return pick_linear<2, 1>(a, group, grid, vec, st);
-  return pick_linear<4, 1>(a, group, grid, vec, st);
+  return rt == 2 ? pick_tokens<2>(a, group, grid, vec, st)
+                 : pick_tokens<1>(a, group, grid, vec, st);
 }
 
 hipError_t launch_q4_quantize(const void* src, int bf16, int N, int K, int64_t ld, int group,

@@ -17,6 +17,12 @@
 // weight operand is the constant -(16 + z) (an integer BF16 holds exactly),
 // which costs no vector instruction and stays below the time of the loads.
 // The group's sum is then multiplied by its scale and added in fp32.
+//
+// The tokens are the instruction's rows and the weights its columns: a lane's
+// results all belong to weight row l % 16, so a group has one scale per lane,
+// and the multiply-adds with it are only as many as a lane has tokens.  Token
+// slot 4 (t % 4) + t / 4 holds token t (result row 4 (l / 16) + i is slot that
+// of lane l's i-th result), so up to four tokens cost one multiply-add, eight two.
 #pragma once
 #include "device.hpp"
 #include "kernels.hpp"
@@ -47,12 +53,16 @@ __device__ __forceinline__ bf16x8 minus_16_plus(uint32_t z) {
   return frag(u32x4{p, p, p, p});
 }
 
-// what a lane holds of one tile: its codes, and per group the scales of the
-// four result rows 4 (l / 16) + i and (ZERO) the zero point of its own row
+// token of operand row r, and the other way round: token of lane l's result i
+__device__ __forceinline__ int slot_token(int r) { return (r >> 2) + 4 * (r & 3); }
+__device__ __forceinline__ int result_token(int lane, int i) { return (lane >> 4) + 4 * i; }
+
+// what a lane holds of one tile: its codes, and per group the scale (and zero
+// point) of its row
 template <int G, bool ZERO>
 struct Tile {
   uint4 codes;
-  uint2 scale[128 / G];
+  uint16_t scale[128 / G];
   uint8_t zero[ZERO ? 128 / G : 1];
 };
 
@@ -68,62 +78,56 @@ __device__ __forceinline__ void load_tile(Tile<G, ZERO>& t, const Matrix& m, int
   const int lane = threadIdx.x & 63;
   const int64_t at = (int64_t)tile * m.nkb + kb;
   t.codes = ldg16(m.codes + (at * 64 + lane) * 16);
+  const int64_t gi = at * (128 / G) * 16 + (lane & 15);
 #pragma unroll
   for (int g = 0; g < 128 / G; ++g) {
-    const int64_t gi = at * (128 / G) + g;
-    t.scale[g] = *reinterpret_cast<const uint2*>(m.scales + gi * 32 + (lane >> 4) * 8);
-    if (ZERO) t.zero[g] = m.zeros[gi * 16 + (lane & 15)];
+    t.scale[g] = *reinterpret_cast<const uint16_t*>(m.scales + (gi + 16 * g) * 2);
+    if (ZERO) t.zero[g] = m.zeros[gi + 16 * g];
   }
 }
 
-// -24 sum x of every group (symmetric matrices: the same for all rows)
-template <int G, int NP>
-__device__ __forceinline__ void group_sums(v4f (&c)[128 / G], const bf16x8 (&x)[NP][4]) {
-  const bf16x8 k = minus_16_plus(8);
-#pragma unroll
-  for (int g = 0; g < 128 / G; ++g) {
-    c[g] = v4f{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int s = g * (G / 32); s < (g + 1) * (G / 32); ++s)
-#pragma unroll
-      for (int p = 0; p < NP; ++p) c[g] = mfma(k, x[p][s], c[g]);
-  }
+__device__ __forceinline__ uint32_t dword(const uint4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
-// acc += this tile times x.  x has NP planes that are summed (a value held as
-// BF16 parts), c is group_sums of them (ZERO: unused).
-template <int G, bool ZERO, int NP>
-__device__ __forceinline__ void mul_tile(v4f& acc, const Tile<G, ZERO>& t,
-                                         const bf16x8 (&w)[4], const bf16x8 (&x)[NP][4],
-                                         const v4f (&c)[128 / G]) {
+// acc[r][j] += x[j] times tile r, for the first TI results of a lane.  Group by
+// group, so that only one group's operands are live.
+template <int RT, int NT, int TI, int G, bool ZERO>
+__device__ __forceinline__ void mul_tiles(float (&acc)[RT][NT][TI], const Tile<G, ZERO> (&t)[RT],
+                                          const bf16x8 (&x)[NT][4]) {
+  constexpr int S = G / 32;
 #pragma unroll
   for (int g = 0; g < 128 / G; ++g) {
-    v4f d = ZERO ? v4f{0.f, 0.f, 0.f, 0.f} : c[g];
-    if (ZERO) {
-      const bf16x8 z = minus_16_plus(t.zero[g]);
+    v4f c[NT];                                        // -24 sum x: for all tiles the same
+    if (!ZERO) {
+      const bf16x8 k = minus_16_plus(8);
 #pragma unroll
-      for (int s = g * (G / 32); s < (g + 1) * (G / 32); ++s)
+      for (int j = 0; j < NT; ++j) {
+        c[j] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int p = 0; p < NP; ++p) d = mfma(z, x[p][s], d);
+        for (int s = 0; s < S; ++s) c[j] = mfma(x[j][g * S + s], k, c[j]);
+      }
     }
 #pragma unroll
-    for (int s = g * (G / 32); s < (g + 1) * (G / 32); ++s)
+    for (int r = 0; r < RT; ++r) {
+      bf16x8 w[S], z;
 #pragma unroll
-      for (int p = 0; p < NP; ++p) d = mfma(w[s], x[p][s], d);
-    const uint2 sc = t.scale[g];
-    acc[0] = fmaf(bf16_lo(sc.x), d[0], acc[0]);
-    acc[1] = fmaf(bf16_hi(sc.x), d[1], acc[1]);
-    acc[2] = fmaf(bf16_lo(sc.y), d[2], acc[2]);
-    acc[3] = fmaf(bf16_hi(sc.y), d[3], acc[3]);
+      for (int s = 0; s < S; ++s) w[s] = codes_plus16(dword(t[r].codes, g * S + s));
+      if (ZERO) z = minus_16_plus(t[r].zero[g]);
+      const float sc = __uint_as_float((uint32_t)t[r].scale[g] << 16);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        v4f d = ZERO ? v4f{0.f, 0.f, 0.f, 0.f} : c[j];
+        if (ZERO)
+#pragma unroll
+          for (int s = 0; s < S; ++s) d = mfma(x[j][g * S + s], z, d);
+#pragma unroll
+        for (int s = 0; s < S; ++s) d = mfma(x[j][g * S + s], w[s], d);
+#pragma unroll
+        for (int i = 0; i < TI; ++i) acc[r][j][i] = fmaf(sc, d[i], acc[r][j][i]);
+      }
+    }
   }
-}
-
-template <int G, bool ZERO>
-__device__ __forceinline__ void tile_weights(bf16x8 (&w)[4], const Tile<G, ZERO>& t) {
-  w[0] = codes_plus16(t.codes.x);
-  w[1] = codes_plus16(t.codes.y);
-  w[2] = codes_plus16(t.codes.z);
-  w[3] = codes_plus16(t.codes.w);
 }
 
 }  // namespace q4

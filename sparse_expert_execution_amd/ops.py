@@ -5,6 +5,7 @@ Every step of the layer runs in libmoe.so's kernels; nothing here computes.
 """
 
 import ctypes
+import functools
 
 import torch
 
@@ -57,27 +58,42 @@ def route(desc, x, w_router, ids, w, ws, stream=None):
 
 def _take(name, t, dtype, shape, device=None, rows=False):
     """Checks one tensor argument: type, shape, contiguity (rows: only the last
-    axis need be), and the device it shares with the others.  Returns its device."""
-    if t.dtype != dtype:
+    axis need be), and that it is on the current device (device None) or with
+    the others (their device's index).  Returns the index."""
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if rows:
-        if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or \
-                (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        if (shape[1] > 1 and t.stride(1) != 1) or (shape[0] > 1 and t.stride(0) < shape[1]):
             raise ValueError(f"{name} must have contiguous rows that do not overlap")
     elif not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
-    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, which is not the current device")
-    return t.device
+    index = t.get_device()
+    if device is None:
+        if index < 0 or index != torch.cuda.current_device():
+            raise ValueError(f"{name} is on {t.device}, which is not the current device")
+    elif index != device:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{device}")
+    return index
 
 
 def _take_ws(ws, device):
     _take("ws", ws, torch.uint8, (ws.numel(),), device)
-    return _ptr(ws), ws.numel()
+    return ws.data_ptr(), ws.numel()
+
+
+def _at(t):
+    return t.data_ptr() if t is not None else None
+
+
+def _on(stream, device):
+    """The stream's handle; the current stream of the device without one."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    if stream.device_index != device:
+        raise ValueError(f"the stream belongs to cuda:{stream.device_index}, not to cuda:{device}")
+    return stream.cuda_stream
 
 
 def router_logits(desc, x, w_router, logits, stream=None):
@@ -86,8 +102,8 @@ def router_logits(desc, x, w_router, logits, stream=None):
     dev = _take("x", x, torch.bfloat16, (T, desc.hidden))
     _take("w_router", w_router, _router_type(desc), (desc.n_experts, desc.hidden), dev)
     _take("logits", logits, torch.float32, (T, desc.n_experts), dev)
-    check(lib().moe_router_logits(ctypes.byref(desc), _ptr(x), _ptr(w_router), T, _ptr(logits),
-                                  _stream(stream)), "moe_router_logits")
+    check(lib().moe_router_logits(ctypes.byref(desc), _at(x), _at(w_router), T, _at(logits),
+                                  _on(stream, dev)), "moe_router_logits")
 
 
 def _router_type(desc):
@@ -110,8 +126,8 @@ def gate(desc, logits, ids, w, ws=None, mask=None, counts=None, loss=None, strea
     if loss is not None:
         _take("loss", loss, torch.float32, (1,), dev)
     wsp, wsn = (None, 0) if ws is None else _take_ws(ws, dev)
-    check(lib().moe_gate(ctypes.byref(desc), _ptr(logits), T, _ptr(mask), _ptr(ids), _ptr(w),
-                         _ptr(counts), _ptr(loss), wsp, wsn, _stream(stream)), "moe_gate")
+    check(lib().moe_gate(ctypes.byref(desc), _at(logits), T, _at(mask), _at(ids), _at(w),
+                         _at(counts), _at(loss), wsp, wsn, _on(stream, dev)), "moe_gate")
 
 
 def gate_backward(desc, logits, ids, w, dlogits, dw=None, counts=None, dloss=None, stream=None):
@@ -128,9 +144,9 @@ def gate_backward(desc, logits, ids, w, dlogits, dw=None, counts=None, dloss=Non
         if t is not None:
             _take(name, t, dt, shape, dev)
     _take("dlogits", dlogits, torch.float32, (T, E), dev)
-    check(lib().moe_gate_backward(ctypes.byref(desc), _ptr(logits), T, _ptr(ids), _ptr(w),
-                                  _ptr(dw), _ptr(counts), _ptr(dloss), _ptr(dlogits),
-                                  _stream(stream)), "moe_gate_backward")
+    check(lib().moe_gate_backward(ctypes.byref(desc), _at(logits), T, _at(ids), _at(w),
+                                  _at(dw), _at(counts), _at(dloss), _at(dlogits),
+                                  _on(stream, dev)), "moe_gate_backward")
 
 
 def router_backward(desc, x, w_router, dlogits, ws, dx=None, dw_router=None, stream=None):
@@ -147,9 +163,9 @@ def router_backward(desc, x, w_router, dlogits, ws, dx=None, dw_router=None, str
     if dw_router is not None:
         _take("dw_router", dw_router, torch.float32, (E, H), dev)
     wsp, wsn = _take_ws(ws, dev)
-    check(lib().moe_router_backward(ctypes.byref(desc), _ptr(x), _ptr(w_router), T,
-                                    _ptr(dlogits), _ptr(dx), _ptr(dw_router), wsp, wsn,
-                                    _stream(stream)), "moe_router_backward")
+    check(lib().moe_router_backward(ctypes.byref(desc), _at(x), _at(w_router), T,
+                                    _at(dlogits), _at(dx), _at(dw_router), wsp, wsn,
+                                    _on(stream, dev)), "moe_router_backward")
 
 
 def decode(desc, x, ids, w, pool, y, ws, slot_of=None, shared=None, stream=None):
@@ -237,8 +253,13 @@ def q4_layout(desc):
     return list(off), n.value
 
 
+@functools.lru_cache(maxsize=1024)
+def _q4_bytes(rows, cols, group, has_zero):
+    return q4_layout(MoeQ4Desc(rows, cols, group, has_zero))[1]
+
+
 def _take_block(desc, block, device):
-    need = q4_layout(desc)[1]
+    need = _q4_bytes(desc.rows, desc.cols, desc.group, desc.has_zero)
     _take("block", block, torch.uint8, (block.numel(),), device)
     if block.numel() < need:
         raise ValueError(f"block has {block.numel()} bytes, the matrix takes {need}")
@@ -251,9 +272,9 @@ def q4_quantize(desc, src, block, stream=None):
         raise TypeError("src must be float32 or bfloat16")
     dev = _take("src", src, src.dtype, (desc.rows, desc.cols), rows=True)
     _take_block(desc, block, dev)
-    check(lib().moe_q4_quantize(ctypes.byref(desc), _ptr(src),
+    check(lib().moe_q4_quantize(ctypes.byref(desc), _at(src),
                                 _lib.WTYPE_F32 if src.dtype == torch.float32 else _lib.WTYPE_BF16,
-                                max(src.stride(0), desc.cols), _ptr(block), _stream(stream)),
+                                max(src.stride(0), desc.cols), _at(block), _on(stream, dev)),
           "moe_q4_quantize")
 
 
@@ -266,8 +287,8 @@ def q4_pack(desc, codes, scales, block, zeros=None, stream=None):
     if zeros is not None:
         _take("zeros", zeros, torch.uint8, (desc.rows, g), dev)
     _take_block(desc, block, dev)
-    check(lib().moe_q4_pack(ctypes.byref(desc), _ptr(codes), _ptr(scales), _ptr(zeros),
-                            _ptr(block), _stream(stream)), "moe_q4_pack")
+    check(lib().moe_q4_pack(ctypes.byref(desc), _at(codes), _at(scales), _at(zeros),
+                            _at(block), _on(stream, dev)), "moe_q4_pack")
 
 
 def q4_linear(desc, x, block, y, stream=None):
@@ -279,10 +300,10 @@ def q4_linear(desc, x, block, y, stream=None):
         raise TypeError("y must be float32 or bfloat16")
     _take("y", y, y.dtype, (T, desc.rows), dev, rows=True)
     _take_block(desc, block, dev)
-    check(lib().moe_q4_linear(ctypes.byref(desc), _ptr(x), max(x.stride(0), desc.cols), T,
-                              _ptr(block), _ptr(y),
+    check(lib().moe_q4_linear(ctypes.byref(desc), _at(x), max(x.stride(0), desc.cols), T,
+                              _at(block), _at(y),
                               _lib.WTYPE_F32 if y.dtype == torch.float32 else _lib.WTYPE_BF16,
-                              max(y.stride(0), desc.rows), _stream(stream)), "moe_q4_linear")
+                              max(y.stride(0), desc.rows), _on(stream, dev)), "moe_q4_linear")
 
 
 def dequant_mxfp4(codes, scales, out, stream=None):
