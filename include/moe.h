@@ -212,9 +212,9 @@ int moe_gate_backward(const moe_desc* desc, const float* logits, int32_t T,
                       void* stream);
 
 /* moe_router_backward: dx = dlogits w_router (BF16, rounded once from fp32)
- * and dw_router = dlogits^T x (fp32), on the BF16 matrix cores with dlogits
- * (and an fp32 w_router) entering as two BF16 parts each, i.e. to within
- * 2^-17.  Sums over tokens are taken in a fixed order.
+ * and dw_router = dlogits^T x (fp32), on the BF16 matrix cores.  dlogits enters
+ * dw_router as three BF16 parts (all 24 bits), and dx as two, as does an fp32
+ * w_router there (to within 2^-16).  Sums are taken in a fixed order.
  *   x         device [T][H] BF16 (may be NULL without dw_router)
  *   w_router  device [E][H] in desc->router_wtype (may be NULL without dx)
  *   dlogits   device [T][E] float
@@ -248,9 +248,9 @@ int moe_router_backward(const moe_desc* desc, const void* x, const void* w_route
  * matrix core by cost: an expert's rows weigh more the more tokens chose
  * it) and each row's gate-weighted result is added into y with an fp32
  * atomic, so the summation order (and the last bits of y) can differ
- * between runs.  INT4 experts: x as given, h held as two BF16 parts (to within
- * 2^-17), fp32 accumulation, two kernels for any T, T * k <= 512, the sums in
- * a fixed order (no atomics on y, no wait between workgroups).
+ * between runs.  INT4 experts: x as given, h in fp32 (handed on as three BF16
+ * parts), fp32 accumulation, all T tokens in one pass, the sums in a fixed order
+ * (no atomics on y, no wait between workgroups).
  *   x              device [T][H] BF16;   1 <= T <= MOE_DECODE_MAX_T
  *   ids, w         device [T][k] (from moe_route or the caller)
  *   slot_of_expert device [E] int32: slot holding expert e, -1 = not

@@ -518,8 +518,9 @@ int moe_router_logits(const moe_desc* desc, const void* x, const void* w_router,
   if (!x || !w_router || !logits) return set_error(MOE_EINVAL, "null pointer");
   if (!aligned(x, 16) || !aligned(w_router, 16) || !aligned(logits, 16))
     return set_error(MOE_EINVAL, "x, w_router and logits must be 16-byte aligned");
-  return hip_status(moe::launch_logits(x, w_router, desc->router_wtype == MOE_WTYPE_F32, T,
-                                       desc->hidden, desc->n_experts, logits, as_stream(stream)),
+  return hip_status(moe::launch_router_logits(x, w_router, desc->router_wtype == MOE_WTYPE_F32, T,
+                                              desc->hidden, desc->n_experts, logits,
+                                              as_stream(stream)),
                     "moe_router_logits");
 }
 

@@ -20,140 +20,204 @@
 namespace moe {
 namespace {
 
-constexpr int kGateWaves = 4;
+constexpr int kGateWaves = 4;     // of the gradient
 
-// Sum over the tokens of a workgroup of p_e and of the choices, in registers
-// (a lane owns experts lane + 64 i), then over its waves in LDS: one partial
-// row per workgroup, so the sums have a fixed order and need no atomics.
-template <int M, bool STATS>
-__global__ __launch_bounds__(kGateWaves * 64) void gate_kernel(GateArgs a) {
-  __shared__ float ls[STATS ? kGateWaves * M * 64 : 1];
-  __shared__ int lc[STATS ? kGateWaves * M * 64 : 1];
-  __shared__ int ln[kGateWaves];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  float S[M];
-  int C[M];
+// e^x for x <= 0 as 2^(x log2 e): the product's rounding error and the constant's
+// are put back (without them the error grows with |x|)
+__device__ __forceinline__ float exp_neg(float x) {
+  constexpr float kL2e = 1.44269502f, kL2eLo = 1.92596299e-8f;
+  const float t = x * kL2e;
+  const float r = fmaf(x, kL2e, -t) + x * kL2eLo;
+  const float e = __builtin_amdgcn_exp2f(t);
+  // below e^-200 the result is 0 in fp32, and r may be an infinity or NaN
+  return x < -200.f ? 0.f : fmaf(e, r * 0.693147181f, e);
+}
+
+// maximum, sum, "or" over the 16 lanes of a DPP row, in every lane of it
+__device__ __forceinline__ float row_max(float v) {
+  v = fmaxf(v, dpp_f<kDppXor1>(v));
+  v = fmaxf(v, dpp_f<kDppXor2>(v));
+  v = fmaxf(v, dpp_f<kDppHalfMirror>(v));
+  return fmaxf(v, dpp_f<kDppMirror>(v));
+}
+__device__ __forceinline__ float row_sum(float v) {
+  v += dpp_f<kDppXor1>(v);
+  v += dpp_f<kDppXor2>(v);
+  v += dpp_f<kDppHalfMirror>(v);
+  return v + dpp_f<kDppMirror>(v);
+}
+__device__ __forceinline__ uint32_t row_max_u32(uint32_t v) {
+  v = max(v, dpp_u<kDppXor1>(v));
+  v = max(v, dpp_u<kDppXor2>(v));
+  v = max(v, dpp_u<kDppHalfMirror>(v));
+  return max(v, dpp_u<kDppMirror>(v));
+}
+__device__ __forceinline__ uint32_t row_min_u32(uint32_t v) {
+  v = min(v, dpp_u<kDppXor1>(v));
+  v = min(v, dpp_u<kDppXor2>(v));
+  v = min(v, dpp_u<kDppHalfMirror>(v));
+  return min(v, dpp_u<kDppMirror>(v));
+}
+
+// A wave takes four tokens at once, 16 lanes each: the reductions stay inside
+// a DPP row (four instructions for four tokens; a token per wave needs them and
+// the steps between rows for each one).  Lane l of a row holds the logits of
+// experts 64 c + 4 l + (0..3), c < C.  Round by round the largest key and the
+// lowest id that holds it are taken out.
+//
+// Statistics: choices are counted in LDS (integers: any order); the sums of p
+// stay in registers over a wave's tokens and are added over its rows, then over
+// the workgroup's waves, in a fixed order: one partial row per workgroup.
+template <int C, int WAVES, int KB, bool STATS>
+__global__ __launch_bounds__(WAVES * 64) void gate_kernel(GateArgs a) {
+  constexpr int V = 4 * C;                            // logits per lane
+  __shared__ float ls[STATS ? WAVES * C * 64 : 1];
+  __shared__ int lc[STATS ? C * 64 + 1 : 1];          // and the tokens routed
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane & 15;
+  if (STATS) {
+    for (int i = threadIdx.x; i <= C * 64; i += WAVES * 64) lc[i] = 0;
+    __syncthreads();
+  }
+  const bool vec = a.E % 4 == 0;
+  float S[V];
 #pragma unroll
-  for (int i = 0; i < M; ++i) { S[i] = 0.f; C[i] = 0; }
-  int routed = 0;
-  for (int64_t t = (int64_t)blockIdx.x * kGateWaves + wave; t < a.T;
-       t += (int64_t)gridDim.x * kGateWaves) {
-    int my_id = -1;
-    float my_w = 0.f;
-    bool live = !a.mask || a.mask[t];
-    if (live) {
-      float v[M];
-      uint32_t key[M];
-      float m = -INFINITY;
-      bool nan = false;
+  for (int i = 0; i < V; ++i) S[i] = 0.f;
+  for (int64_t t0 = ((int64_t)wave * gridDim.x + blockIdx.x) * 4; t0 < a.T;
+       t0 += (int64_t)gridDim.x * WAVES * 4) {
+    const int64_t t = t0 + (lane >> 4);
+    const bool in = t < a.T && (!a.mask || a.mask[t]);
+    float v[V];
 #pragma unroll
-      for (int i = 0; i < M; ++i) {
-        const int e = lane + 64 * i;
-        // + 0: a logit of -0 ranks with +0
-        v[i] = e < a.E ? a.z[t * a.E + e] + 0.f : -INFINITY;
-        nan |= v[i] != v[i];
-        key[i] = v[i] > -INFINITY ? fkey(v[i]) : 0u;   // 0: never chosen (-inf, NaN)
-        m = fmaxf(m, v[i]);
-      }
-      m = wave_max_dpp(m);
-      if (m == -INFINITY && __ballot(nan) == 0) {
-        live = false;                                  // no expert is available
+    for (int c = 0; c < C; ++c) {
+      const int e = 64 * c + 4 * l;
+      const float* src = a.z + t * a.E + e;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[4 * c + i] = -INFINITY;
+      if (vec) {
+        if (in && e < a.E) {
+          const float4 f = *reinterpret_cast<const float4*>(src);
+          v[4 * c] = f.x; v[4 * c + 1] = f.y; v[4 * c + 2] = f.z; v[4 * c + 3] = f.w;
+        }
       } else {
-        float p[M], ps = 0.f;
 #pragma unroll
-        for (int i = 0; i < M; ++i) {
-          p[i] = lane + 64 * i < a.E ? expf(v[i] - m) : 0.f;
-          ps += p[i];
-        }
-        const float inv = 1.0f / wave_sum_dpp(ps);
-        float wsum = 0.f;
-        for (int j = 0; j < a.k; ++j) {
-          uint32_t lb = 0;
-          int li = 0;
+        for (int i = 0; i < 4; ++i)
+          if (in && e + i < a.E) v[4 * c + i] = src[i];
+      }
+    }
+    float m = -INFINITY;
+    uint32_t nan = 0;
 #pragma unroll
-          for (int i = 0; i < M; ++i)
-            if (key[i] > lb) { lb = key[i]; li = i; }
-          const uint32_t gm = wave_max_u32_dpp(lb);
-          if (gm == 0) break;
-          uint64_t win = __ballot(lb == gm);
-          int id = 0x7fffffff;
-          while (win) {
-            const int l = __builtin_ctzll(win);
-            const int cand = l + 64 * __builtin_amdgcn_readlane(li, l);
-            id = cand < id ? cand : id;
-            win &= win - 1;
-          }
+    for (int i = 0; i < V; ++i) {
+      v[i] += 0.f;                                    // a logit of -0 ranks with +0
+      nan |= v[i] != v[i];
+      m = fmaxf(m, v[i]);
+    }
+    m = row_max(m);
+    // a row with no expert available (or masked, or past the end) is not routed
+    const bool routed = in && (m > -INFINITY || row_max_u32(nan));
+    // the maximum a row subtracts: any finite one will do where nothing is routed
+    const float sub = routed ? m : 0.f;
+    uint32_t key[V];
+    float ps = 0.f;
 #pragma unroll
-          for (int i = 0; i < M; ++i)
-            if (lane + 64 * i == id) {
-              key[i] = 0u;
-              if (STATS) ++C[i];
-            }
-          const float e = expf(fkey_value(gm) - m);
-          wsum += e;
-          if (lane == j) { my_w = e; my_id = id; }
-        }
-        // without an expert to choose (a row of NaN) the ids stay -1; a NaN in
-        // the row makes its weights NaN through inv
-        my_w = my_id < 0 ? 0.f : a.renorm ? my_w / (wsum + 0.f * inv) : my_w * inv;
-        if (STATS) {
+    for (int i = 0; i < V; ++i) {
+      key[i] = v[i] > -INFINITY ? fkey(v[i]) : 0u;    // 0: never chosen (-inf, NaN)
+      v[i] = exp_neg(v[i] - sub);
+      ps += v[i];
+    }
+    const float inv = 1.0f / row_sum(ps);             // not routed: infinite, not used
+    if (STATS) {
 #pragma unroll
-          for (int i = 0; i < M; ++i) S[i] += p[i] * inv;
-          ++routed;
+      for (int i = 0; i < V; ++i) S[i] += routed ? v[i] * inv : 0.f;
+      if (routed && l == 0) atomicAdd(&lc[C * 64], 1);
+    }
+    int rid[KB];
+    float rw[KB], wsum = 0.f;
+#pragma unroll
+    for (int b = 0; b < KB; ++b) {
+      rid[b] = -1;
+      rw[b] = 0.f;
+      for (int j = 0; j < 16 && 16 * b + j < a.k; ++j) {
+        uint32_t best = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) best = max(best, key[i]);
+        const uint32_t gm = row_max_u32(best);
+        uint32_t id = 0xffffffffu;
+#pragma unroll
+        for (int i = V - 1; i >= 0; --i)
+          if (key[i] == gm) id = 64 * (i / 4) + 4 * l + i % 4;
+        id = row_min_u32(id);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (64u * (i / 4) + 4 * l + i % 4 == id) key[i] = 0u;
+        const bool have = gm != 0u;                   // an expert is left
+        const float e = have ? exp_neg(fkey_value(gm) - sub) : 0.f;
+        wsum += e;
+        if (l == j) {
+          rid[b] = have ? (int)id : -1;
+          rw[b] = e;
+          if (STATS && have) atomicAdd(&lc[id], 1);
         }
       }
     }
-    if (lane < a.k) {
-      a.ids[t * a.k + lane] = live ? my_id : -1;
-      a.w[t * a.k + lane] = live ? my_w : 0.f;
+    if (t < a.T) {
+#pragma unroll
+      for (int b = 0; b < KB; ++b)
+        if (16 * b + l < a.k) {
+          // a NaN in the row makes its weights NaN through inv
+          const float w = a.renorm ? rw[b] / (wsum + 0.f * inv) : rw[b] * inv;
+          a.ids[t * a.k + 16 * b + l] = routed ? rid[b] : -1;
+          a.w[t * a.k + 16 * b + l] = routed && rid[b] >= 0 ? w : 0.f;
+        }
     }
   }
   if (STATS) {
 #pragma unroll
-    for (int i = 0; i < M; ++i) {
-      ls[(wave * M + i) * 64 + lane] = S[i];
-      lc[(wave * M + i) * 64 + lane] = C[i];
+    for (int i = 0; i < V; ++i) {
+      S[i] += __shfl_xor(S[i], 16, kWave);
+      S[i] += __shfl_xor(S[i], 32, kWave);
     }
-    if (lane == 0) ln[wave] = routed;
-    __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += kGateWaves * 64) {
-      float s = 0.f;
-      int c = 0;
+    if (lane < 16) {
 #pragma unroll
-      for (int w = 0; w < kGateWaves; ++w) {
-        s += ls[w * M * 64 + e];
-        c += lc[w * M * 64 + e];
-      }
+      for (int c = 0; c < C; ++c)
+        *reinterpret_cast<v4f*>(&ls[wave * C * 64 + 64 * c + 4 * l]) =
+            v4f{S[4 * c], S[4 * c + 1], S[4 * c + 2], S[4 * c + 3]};
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += WAVES * 64) {
+      float s = 0.f;
+      for (int w = 0; w < WAVES; ++w) s += ls[w * C * 64 + e];
       a.part_s[(int64_t)blockIdx.x * a.E + e] = s;
-      a.part_c[(int64_t)blockIdx.x * a.E + e] = c;
+      a.part_c[(int64_t)blockIdx.x * a.E + e] = lc[e];
     }
     if (threadIdx.x == 0) {
-      int r = 0;
-#pragma unroll
-      for (int w = 0; w < kGateWaves; ++w) r += ln[w];
-      a.part_n[blockIdx.x] = r;
-      if (blockIdx.x == 0) *a.ticket = 0u;             // for gate_reduce_kernel, the next launch
+      a.part_n[blockIdx.x] = lc[C * 64];
+      if (blockIdx.x == 0) *a.ticket = 0u;            // for gate_reduce_kernel, the next launch
     }
   }
 }
 
-// Partial rows -> counts and the loss.  A workgroup takes 64 experts (4 slices
-// of the rows each); the last one to finish adds the workgroups' shares of
-// the loss in order.
-__global__ __launch_bounds__(256) void gate_reduce_kernel(GateArgs a, int parts) {
-  __shared__ float ss[4][64];
-  __shared__ int sc[4][64];
-  __shared__ int sn[4];
+// Partial rows -> counts and the loss.  A workgroup takes 64 experts, its 16
+// waves every 16th row each; the last workgroup to finish adds the
+// workgroups' shares of the loss in order.
+constexpr int kReduceWaves = 16;
+
+__global__ __launch_bounds__(kReduceWaves * 64) void gate_reduce_kernel(GateArgs a, int parts) {
+  __shared__ float ss[kReduceWaves][64];
+  __shared__ int sc[kReduceWaves][64];
+  __shared__ int sn[kReduceWaves];
   const int lane = threadIdx.x & 63, q = threadIdx.x >> 6;
   const int e = blockIdx.x * 64 + lane;
   float s = 0.f;
   int c = 0, n = 0;
-  if (e < a.E)
-    for (int b = q; b < parts; b += 4) {
+  if (e < a.E) {
+#pragma unroll 8
+    for (int b = q; b < parts; b += kReduceWaves) {
       s += a.part_s[(int64_t)b * a.E + e];
       c += a.part_c[(int64_t)b * a.E + e];
     }
-  for (int b = threadIdx.x; b < parts; b += 256) n += a.part_n[b];
+  }
+  for (int b = threadIdx.x; b < parts; b += kReduceWaves * 64) n += a.part_n[b];
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) n += __shfl_xor(n, off, kWave);
   ss[q][lane] = s;
@@ -161,9 +225,15 @@ __global__ __launch_bounds__(256) void gate_reduce_kernel(GateArgs a, int parts)
   if (lane == 0) sn[q] = n;
   __syncthreads();
   if (q != 0) return;
-  n = sn[0] + sn[1] + sn[2] + sn[3];
-  s = (ss[0][lane] + ss[1][lane]) + (ss[2][lane] + ss[3][lane]);
-  c = sc[0][lane] + sc[1][lane] + sc[2][lane] + sc[3][lane];
+  n = 0;
+  s = 0.f;
+  c = 0;
+#pragma unroll
+  for (int w = 0; w < kReduceWaves; ++w) {
+    n += sn[w];
+    s += ss[w][lane];
+    c += sc[w][lane];
+  }
   if (a.counts) {
     if (e < a.E) a.counts[e] = c;
     if (blockIdx.x == 0 && lane == 0) a.counts[a.E] = n;
@@ -256,26 +326,33 @@ __global__ __launch_bounds__(kGateWaves * 64) void gate_backward_kernel(GateBack
   }
 }
 
-template <int M>
-hipError_t run_gate(const GateArgs& a, int grid, hipStream_t st) {
+template <int C, int WAVES, int KB>
+hipError_t run_gate_k(const GateArgs& a, int grid, hipStream_t st) {
   if (a.counts || a.loss)
-    hipLaunchKernelGGL((gate_kernel<M, true>), dim3(grid), dim3(kGateWaves * 64), 0, st, a);
+    hipLaunchKernelGGL((gate_kernel<C, WAVES, KB, true>), dim3(grid), dim3(WAVES * 64), 0, st, a);
   else
-    hipLaunchKernelGGL((gate_kernel<M, false>), dim3(grid), dim3(kGateWaves * 64), 0, st, a);
+    hipLaunchKernelGGL((gate_kernel<C, WAVES, KB, false>), dim3(grid), dim3(WAVES * 64), 0, st, a);
   return hipGetLastError();
+}
+
+template <int C, int WAVES>
+hipError_t run_gate(const GateArgs& a, int grid, hipStream_t st) {
+  return a.k <= 16 ? run_gate_k<C, WAVES, 1>(a, grid, st) : run_gate_k<C, WAVES, 4>(a, grid, st);
 }
 
 }  // namespace
 
 hipError_t launch_gate(const GateArgs& a, hipStream_t st) {
   const int grid = gate_parts(a.T);
-  hipError_t err = a.E <= 64    ? run_gate<1>(a, grid, st)
-                   : a.E <= 128 ? run_gate<2>(a, grid, st)
-                   : a.E <= 256 ? run_gate<4>(a, grid, st)
-                   : a.E <= 512 ? run_gate<8>(a, grid, st)
-                                : run_gate<16>(a, grid, st);
+  // waves per workgroup: as many as the registers of a lane's logits allow
+  hipError_t err = a.E <= 64    ? run_gate<1, 16>(a, grid, st)
+                   : a.E <= 128 ? run_gate<2, 16>(a, grid, st)
+                   : a.E <= 256 ? run_gate<4, 16>(a, grid, st)
+                   : a.E <= 512 ? run_gate<8, 8>(a, grid, st)
+                                : run_gate<16, 4>(a, grid, st);
   if (err != hipSuccess || !(a.counts || a.loss)) return err;
-  hipLaunchKernelGGL(gate_reduce_kernel, dim3((a.E + 63) / 64), dim3(256), 0, st, a, grid);
+  hipLaunchKernelGGL(gate_reduce_kernel, dim3((a.E + 63) / 64), dim3(kReduceWaves * 64), 0, st, a,
+                     grid);
   return hipGetLastError();
 }
 

@@ -81,10 +81,6 @@ hipError_t launch_route_large(const void* x, const void* w_router, int router_f3
                               int H, int E, int k, int renorm, float* logits, int32_t* ids,
                               float* w, hipStream_t st);
 
-// logits alone, the first launch of launch_route_large
-hipError_t launch_logits(const void* x, const void* w_router, int router_f32, int T, int H, int E,
-                         float* logits, hipStream_t st);
-
 // the gate on given logits, its statistics and its gradient (gate.hip)
 struct GateArgs {
   const float* z;          // [T][E]
@@ -101,8 +97,8 @@ struct GateArgs {
   float* share;            // [16]
   unsigned* ticket;
 };
-// workgroups (and rows of partial sums) of the gate: 4 tokens each until 256
-inline int gate_parts(int T) { return T < 1024 ? (T + 3) / 4 : 256; }
+// workgroups (and rows of partial sums) of the gate: 16 tokens each until 256
+inline int gate_parts(int T) { return T < 4096 ? (T + 15) / 16 : 256; }
 hipError_t launch_gate(const GateArgs& a, hipStream_t st);
 
 struct GateBackward {
@@ -117,7 +113,9 @@ struct GateBackward {
 };
 hipError_t launch_gate_backward(const GateBackward& a, hipStream_t st);
 
-// gradients of the router's product (router_train.hip)
+// the router's product alone, and its gradients (router_train.hip)
+hipError_t launch_router_logits(const void* x, const void* w, int router_f32, int T, int H, int E,
+                                float* z, hipStream_t st);
 struct RouterBackward {
   const void* x;           // BF16 [T][H]
   const void* w;           // [E][H]

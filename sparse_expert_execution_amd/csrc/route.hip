@@ -192,8 +192,9 @@ __global__ __launch_bounds__(256) void topk_kernel(const float* __restrict__ z, 
 
 }  // namespace
 
-hipError_t launch_logits(const void* x, const void* w_router, int router_f32, int T, int H, int E,
-                         float* logits, hipStream_t st) {
+hipError_t launch_route_large(const void* x, const void* w_router, int router_f32, int T,
+                              int H, int E, int k, int renorm, float* logits, int32_t* ids,
+                              float* w, hipStream_t st) {
   dim3 grid((T + 63) / 64, (E + 63) / 64);
   const uint16_t* xb = static_cast<const uint16_t*>(x);
   if (!router_f32 && H % 64 == 0)
@@ -205,13 +206,7 @@ hipError_t launch_logits(const void* x, const void* w_router, int router_f32, in
   else
     hipLaunchKernelGGL((logits_tiled_kernel<false>), grid, dim3(256), 0, st, xb, w_router, T, H,
                        E, logits);
-  return hipGetLastError();
-}
-
-hipError_t launch_route_large(const void* x, const void* w_router, int router_f32, int T,
-                              int H, int E, int k, int renorm, float* logits, int32_t* ids,
-                              float* w, hipStream_t st) {
-  const hipError_t err = launch_logits(x, w_router, router_f32, T, H, E, logits, st);
+  hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   const dim3 g((T + 3) / 4), b(256);
   if (E <= 64) hipLaunchKernelGGL(topk_kernel<1>, g, b, 0, st, logits, T, E, k, renorm, ids, w);

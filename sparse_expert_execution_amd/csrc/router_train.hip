@@ -1,11 +1,11 @@
-// router_train.hip - the gradient of the router's product z = x W^T:
+// router_train.hip - the router's product z = x W^T and its gradient:
 //   dx = dz W (BF16)         [T][H] = [T][E] [E][H]
 //   dW = dz^T x (fp32)       [E][H] = [E][T] [T][H]
 //
-// Both run on the BF16 matrix cores with fp32 accumulation.  dz (fp32) enters
-// as two BF16 parts, dz to within 2^-17 of itself (rounding it to one would
-// put 2^-9 of error into an fp32 gradient); an fp32 W does too, and the
-// product of the two small parts is left out.
+// All of it runs on the BF16 matrix cores with fp32 accumulation.  Where the
+// result is fp32 (z, dW), an fp32 factor enters as three BF16 parts, all its 24
+// bits; where it is rounded to BF16 (dx), as two, to within 2^-16, and the
+// product of two small parts is left out.
 //
 // dx is computed transposed, rows h, columns tokens, so that a lane ends up
 // with 16 consecutive h of one token: rows r = 4 q + i of the four 16-row
@@ -32,6 +32,159 @@ __device__ __forceinline__ void split8(const float (&v)[8], u32x4& hi, u32x4& lo
     hi[i] = h;
     lo[i] = l;
   }
+}
+
+// three parts: all 24 bits
+__device__ __forceinline__ void split8x3(const float (&v)[8], u32x4& hi, u32x4& mid, u32x4& lo) {
+  float r[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const v2bf h = {(__bf16)v[2 * i], (__bf16)v[2 * i + 1]};
+    hi[i] = __builtin_bit_cast(uint32_t, h);
+    r[2 * i] = v[2 * i] - bf16_lo(hi[i]);
+    r[2 * i + 1] = v[2 * i + 1] - bf16_hi(hi[i]);
+  }
+  split8(r, mid, lo);
+}
+
+// ---- logits -------------------------------------------------------------------
+// z = x W^T, computed transposed: rows are experts (row r = 4 q + i of tile j of
+// a block of 16 ET is expert 4 ET q + 4 j + i, so a lane ends up with 4 ET
+// consecutive experts of a token), columns tokens.  Both operands have H in
+// order, so they go straight from memory into the operand registers.
+//
+// A workgroup is 8 waves: EW of them side by side over blocks of 16 ET experts,
+// all on the same 16 NT tokens (whose x the others find in L1), and 8 / EW
+// slices of H, whose sums meet in LDS in slice order.  D - 1 steps of 32 h are
+// in flight per wave.  An fp32 W is split into three BF16 parts in registers
+// (all 24 bits; BF16 products are exact, so z is an fp32 sum of exact terms).
+constexpr int kLgWaves = 8;
+
+template <int NT, int ET, bool RF32, int D>
+__global__ __launch_bounds__(kLgWaves * 64, 2) void router_logits_kernel(
+    const uint16_t* __restrict__ x, const void* __restrict__ w, int T, int H, int E, int log_ew,
+    float* __restrict__ z) {
+  extern __shared__ v4f lred[];                       // [slice - 1][e wave][ET * NT][64]
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, q = lane >> 4;
+  const int EW = 1 << log_ew, ew = wave & (EW - 1), slice = wave >> log_ew;
+  const int KW = kLgWaves >> log_ew;
+  const int64_t t0 = (int64_t)blockIdx.x * 16 * NT;
+  const int e0 = ((int)blockIdx.y * EW + ew) * 16 * ET;
+  const int steps = H / 32, n_it = slice < steps ? (steps - slice + KW - 1) / KW : 0;
+
+  // rows past the end read the last one; their results are not stored
+  const uint16_t* xp[NT];
+  int64_t wo[ET];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const int64_t t = t0 + 16 * j + r;
+    xp[j] = x + (t < T ? t : T - 1) * H + 8 * q;
+  }
+#pragma unroll
+  for (int j = 0; j < ET; ++j) {
+    const int e = e0 + 4 * ET * (r >> 2) + 4 * j + (r & 3);
+    wo[j] = (int64_t)(e < E ? e : E - 1) * H + 8 * q;
+  }
+  struct Step {
+    u32x4 x[NT];
+    u32x4 w[ET][RF32 ? 2 : 1];
+  };
+  auto load = [&](Step& s, int it) {
+    const int k = 32 * (slice + (it < n_it ? it : n_it - 1) * KW);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) s.x[j] = *reinterpret_cast<const u32x4*>(xp[j] + k);
+#pragma unroll
+    for (int j = 0; j < ET; ++j) {
+      if (RF32) {
+        const u32x4* p =
+            reinterpret_cast<const u32x4*>(static_cast<const float*>(w) + wo[j] + k);
+        s.w[j][0] = p[0];
+        s.w[j][RF32 ? 1 : 0] = p[1];
+      } else {
+        s.w[j][0] =
+            *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(w) + wo[j] + k);
+      }
+    }
+  };
+  v4f acc[ET][NT];
+#pragma unroll
+  for (int e = 0; e < ET; ++e)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[e][j] = v4f{0.f, 0.f, 0.f, 0.f};
+  if (n_it > 0) {
+    Step s[D];
+#pragma unroll
+    for (int d = 0; d < D - 1; ++d) load(s[d], d);
+    for (int i0 = 0; i0 < n_it; i0 += D) {
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        if (i0 + d >= n_it) break;
+        load(s[(d + D - 1) % D], i0 + d + D - 1);     // past the end: the last again
+#pragma unroll
+        for (int e = 0; e < ET; ++e) {
+          if (RF32) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(s[d].w[e][i / 4 * RF32][i % 4]);
+            u32x4 hi, mid, lo;
+            split8x3(v, hi, mid, lo);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+              acc[e][j] = mfma(lo, s[d].x[j], acc[e][j]);
+              acc[e][j] = mfma(mid, s[d].x[j], acc[e][j]);
+              acc[e][j] = mfma(hi, s[d].x[j], acc[e][j]);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < NT; ++j) acc[e][j] = mfma(s[d].w[e][0], s[d].x[j], acc[e][j]);
+          }
+        }
+      }
+    }
+  }
+  if (slice > 0) {
+#pragma unroll
+    for (int e = 0; e < ET; ++e)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        lred[(((slice - 1) * EW + ew) * ET * NT + e * NT + j) * 64 + lane] = acc[e][j];
+  }
+  __syncthreads();
+  if (slice > 0) return;
+  for (int k = 0; k < KW - 1; ++k)
+#pragma unroll
+    for (int e = 0; e < ET; ++e)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        acc[e][j] += lred[((k * EW + ew) * ET * NT + e * NT + j) * 64 + lane];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const int64_t t = t0 + 16 * j + r;
+    if (t >= T) continue;
+#pragma unroll
+    for (int e = 0; e < ET; ++e) {
+      const int c = e0 + 4 * ET * q + 4 * e;
+      float* o = z + t * E + c;
+      if (E % 4 == 0) {
+        if (c < E) *reinterpret_cast<v4f*>(o) = acc[e][j];
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (c + i < E) o[i] = acc[e][j][i];
+      }
+    }
+  }
+}
+
+template <int NT, int ET, bool RF32, int D>
+hipError_t run_logits(const void* x, const void* w, int T, int H, int E, int log_ew, float* z,
+                      hipStream_t st) {
+  const int ew = 1 << log_ew;
+  const dim3 g((T + 16 * NT - 1) / (16 * NT), (E + 16 * ET * ew - 1) / (16 * ET * ew));
+  const size_t lds = (size_t)(kLgWaves - ew) * ET * NT * 64 * sizeof(v4f);
+  hipLaunchKernelGGL((router_logits_kernel<NT, ET, RF32, D>), g, dim3(kLgWaves * 64), lds, st,
+                     static_cast<const uint16_t*>(x), w, T, H, E, log_ew, z);
+  return hipGetLastError();
 }
 
 // ---- W in operand order: [chunk of 64 h][32 e][tile j][part][64 lanes] -------
@@ -153,6 +306,10 @@ __global__ __launch_bounds__(kDxWaves * 64) void router_dx_kernel(const float* _
 }
 
 // ---- dz^T in operand order: [32 tokens][16 e][part][64 lanes] -----------------
+// Three parts here: dW is fp32, and with two its error was 2.5e-6 of its norm
+// where an fp32 product has 5e-7.
+constexpr int kZp = 3;
+
 __global__ __launch_bounds__(256) void pack_dz_kernel(const float* __restrict__ dz, int T, int E,
                                                       int net, u32x4* __restrict__ out) {
   const int64_t kt = blockIdx.x;
@@ -165,11 +322,12 @@ __global__ __launch_bounds__(256) void pack_dz_kernel(const float* __restrict__ 
       const int64_t t = 32 * kt + 8 * kq + j;
       v[j] = t < T && e < E ? dz[t * E + e] : 0.f;
     }
-    u32x4 hi, lo;
-    split8(v, hi, lo);
-    u32x4* o = out + ((kt * net + e / 16) * 2) * 64 + 16 * kq + e % 16;
+    u32x4 hi, mid, lo;
+    split8x3(v, hi, mid, lo);
+    u32x4* o = out + ((kt * net + e / 16) * kZp) * 64 + 16 * kq + e % 16;
     o[0] = hi;
-    o[64] = lo;
+    o[64] = mid;
+    o[128] = lo;
   }
 }
 
@@ -189,17 +347,17 @@ __device__ __forceinline__ uint32_t pack_hi(uint32_t a, uint32_t b) {
 }
 
 template <int ET>
-__global__ __launch_bounds__(kDwWaves * 64) void router_dw_kernel(
+__global__ __launch_bounds__(kDwWaves * 64, 2) void router_dw_kernel(
     const uint16_t* __restrict__ x, const u32x4* __restrict__ zf, int T, int H, int E, int net,
     int per_slice, float* __restrict__ out) {
-  constexpr int kStage = ET * 2 * 64, kCopies = (kStage + kDwWaves * 64 - 1) / (kDwWaves * 64);
+  constexpr int kStage = ET * kZp * 64, kCopies = (kStage + kDwWaves * 64 - 1) / (kDwWaves * 64);
   __shared__ u32x4 sa[2][kStage];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, q = lane >> 4;
   const int nkt = (T + 31) / 32;
   const int k0 = blockIdx.z * per_slice, k1 = min(nkt, k0 + per_slice);
   const int h = blockIdx.x * 256 + wave * 64 + 4 * n;
   const bool hin = h < H;
-  const u32x4* zsrc = zf + (int64_t)blockIdx.y * ET * 2 * 64;
+  const u32x4* zsrc = zf + (int64_t)blockIdx.y * ET * kZp * 64;
 
   u32x4 za[kCopies];
   uint2 xr[8];
@@ -207,7 +365,7 @@ __global__ __launch_bounds__(kDwWaves * 64) void router_dw_kernel(
 #pragma unroll
     for (int c = 0; c < kCopies; ++c) {
       const int i = c * kDwWaves * 64 + threadIdx.x;
-      if (i < kStage) za[c] = zsrc[(int64_t)kt * net * 2 * 64 + i];
+      if (i < kStage) za[c] = zsrc[(int64_t)kt * net * kZp * 64 + i];
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -246,11 +404,11 @@ __global__ __launch_bounds__(kDwWaves * 64) void router_dw_kernel(
     __syncthreads();                                  // this step's dz is in LDS
 #pragma unroll
     for (int e = 0; e < ET; ++e) {
-      const u32x4 hi = sa[buf][(e * 2) * 64 + lane], lo = sa[buf][(e * 2 + 1) * 64 + lane];
 #pragma unroll
-      for (int f = 0; f < 4; ++f) {
-        acc[e][f] = mfma(hi, b[f], acc[e][f]);
-        acc[e][f] = mfma(lo, b[f], acc[e][f]);
+      for (int p = kZp - 1; p >= 0; --p) {            // small parts first
+        const u32x4 z = sa[buf][(e * kZp + p) * 64 + lane];
+#pragma unroll
+        for (int f = 0; f < 4; ++f) acc[e][f] = mfma(z, b[f], acc[e][f]);
       }
     }
     // the other buffer was last read a step ago, before this step's barrier
@@ -280,20 +438,21 @@ __global__ __launch_bounds__(256) void sum_slices_kernel(const v4f* __restrict__
 }
 
 // experts per dW workgroup in tiles of 16, the number of those tiles, and the
-// token slices: enough workgroups for two per compute unit, a slice no
-// shorter than 8 steps of 32 tokens
+// token slices: two workgroups per compute unit where a slice has at least 8
+// steps of 32 tokens; short batches take fewer experts a workgroup instead
 struct DwPlan {
   int et, net, slices, per_slice;
 };
 DwPlan dw_plan(int T, int H, int E) {
   DwPlan p;
+  const int nkt = T > 0 ? (T + 31) / 32 : 1, hx = (H + 255) / 256;
+  const int most = nkt / 8 > 1 ? nkt / 8 : 1;
   p.et = E > 64 ? 8 : E > 32 ? 4 : E > 16 ? 2 : 1;
-  const int ey = (E + 16 * p.et - 1) / (16 * p.et);
+  while (p.et > 1 && hx * ((E + 16 * p.et - 1) / (16 * p.et)) * most < 192) p.et /= 2;
+  const int ey = (E + 16 * p.et - 1) / (16 * p.et), tiles = ey * hx;
   p.net = ey * p.et;
-  const int nkt = T > 0 ? (T + 31) / 32 : 1, tiles = ey * ((H + 255) / 256);
   int s = (512 + tiles - 1) / tiles;
-  if (s > nkt / 8) s = nkt / 8;
-  if (s < 1) s = 1;
+  if (s > most) s = most;
   p.per_slice = (nkt + s - 1) / s;
   p.slices = (nkt + p.per_slice - 1) / p.per_slice;
   return p;
@@ -309,7 +468,7 @@ Ws carve(int T, int H, int E) {
   Ws w;
   size_t o = 0;
   w.wf = o; o = up256(o + (size_t)((H + 63) / 64) * ((E + 31) / 32) * 4 * 2 * 1024);
-  w.zf = o; o = up256(o + (size_t)((T + 31) / 32) * p.net * 2 * 1024);
+  w.zf = o; o = up256(o + (size_t)((T + 31) / 32) * p.net * kZp * 1024);
   w.part = o; o = up256(o + (p.slices > 1 ? (size_t)p.slices * E * H * 4 : 0));
   w.total = o;
   return w;
@@ -338,6 +497,28 @@ hipError_t run_dx(const RouterBackward& a, const u32x4* wf, hipStream_t st) {
 }
 
 }  // namespace
+
+hipError_t launch_router_logits(const void* x, const void* w, int router_f32, int T, int H, int E,
+                                float* z, hipStream_t st) {
+  // The widest tile that still gives 192 workgroups (3/4 of the compute units):
+  // 64 tokens x 256 experts reads x once and W for every 64 tokens; then fewer
+  // experts (more slices of H per workgroup), fewer tokens, last 16 x 16.
+  const auto blocks = [&](int tokens, int experts) {
+    return (int64_t)((T + tokens - 1) / tokens) * ((E + experts - 1) / experts);
+  };
+  for (int log_ew = E > 128 ? 2 : E > 64 ? 1 : 0; log_ew >= 0; --log_ew)
+    if (blocks(64, 64 << log_ew) >= 192)
+      return router_f32 ? run_logits<4, 4, true, 2>(x, w, T, H, E, log_ew, z, st)
+                        : run_logits<4, 4, false, 3>(x, w, T, H, E, log_ew, z, st);
+  if (blocks(32, 64) >= 192)
+    return router_f32 ? run_logits<2, 4, true, 2>(x, w, T, H, E, 0, z, st)
+                      : run_logits<2, 4, false, 3>(x, w, T, H, E, 0, z, st);
+  if (blocks(16, 64) >= 192)
+    return router_f32 ? run_logits<1, 4, true, 2>(x, w, T, H, E, 0, z, st)
+                      : run_logits<1, 4, false, 3>(x, w, T, H, E, 0, z, st);
+  return router_f32 ? run_logits<1, 1, true, 4>(x, w, T, H, E, 0, z, st)
+                    : run_logits<1, 1, false, 4>(x, w, T, H, E, 0, z, st);
+}
 
 size_t router_backward_bytes(int T, int H, int E) { return carve(T, H, E).total; }
 
