@@ -48,122 +48,219 @@ __device__ __forceinline__ void split8x3(const float (&v)[8], u32x4& hi, u32x4& 
 }
 
 // ---- logits -------------------------------------------------------------------
-// z = x W^T, computed transposed: rows are experts (row r = 4 q + i of tile j of
-// a block of 16 ET is expert 4 ET q + 4 j + i, so a lane ends up with 4 ET
-// consecutive experts of a token), columns tokens.  Both operands have H in
-// order, so they go straight from memory into the operand registers.
+// z = x W^T.  Rows of x and W go through LDS: a copy instruction must take
+// consecutive lanes along a row (read straight into operand registers, where
+// neighbouring lanes are different rows, every lane costs a cache lookup of its
+// own: 131 us where T = 16384, H = 4096, E = 256, whatever the line coverage).
 //
-// A workgroup is 8 waves: EW of them side by side over blocks of 16 ET experts,
-// all on the same 16 NT tokens (whose x the others find in L1), and 8 / EW
-// slices of H, whose sums meet in LDS in slice order.  D - 1 steps of 32 h are
-// in flight per wave.  An fp32 W is split into three BF16 parts in registers
-// (all 24 bits; BF16 products are exact, so z is an fp32 sum of exact terms).
+// A workgroup is 8 waves on TM tokens x TE experts, 32 KS h per stage, STAGES
+// stages in LDS, copied STAGES - 1 ahead (global to LDS, no registers).  Piece
+// p (16 bytes) of row i sits at slot p ^ (i / 2) % 8 of a 128-byte row, p ^ i % 16
+// of a longer one, so that the 16 rows of an operand read hit distinct banks.  A
+// wave takes 16 WT tokens x 16 WE experts of one or more 32-h steps of the
+// stage; the sums of the waves along h meet in LDS in order.
+//
+// The result is transposed, rows experts: row r = 4 q + i of tile j of a wave's
+// experts is expert 4 WE q + 4 j + i, so a lane stores 4 WE consecutive ones.
+// An fp32 W is split into three BF16 parts in registers (all 24 bits; BF16
+// products are exact, so z is an fp32 sum of exact terms).
 constexpr int kLgWaves = 8;
 
-template <int NT, int ET, bool RF32, int D>
-__global__ __launch_bounds__(kLgWaves * 64, 2) void router_logits_kernel(
-    const uint16_t* __restrict__ x, const void* __restrict__ w, int T, int H, int E, int log_ew,
-    float* __restrict__ z) {
-  extern __shared__ v4f lred[];                       // [slice - 1][e wave][ET * NT][64]
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, q = lane >> 4;
-  const int EW = 1 << log_ew, ew = wave & (EW - 1), slice = wave >> log_ew;
-  const int KW = kLgWaves >> log_ew;
-  const int64_t t0 = (int64_t)blockIdx.x * 16 * NT;
-  const int e0 = ((int)blockIdx.y * EW + ew) * 16 * ET;
-  const int steps = H / 32, n_it = slice < steps ? (steps - slice + KW - 1) / KW : 0;
+__device__ __forceinline__ uint32_t lds_addr(const void* p) {
+  return (uint32_t)(uintptr_t)p;
+}
 
-  // rows past the end read the last one; their results are not stored
-  const uint16_t* xp[NT];
-  int64_t wo[ET];
+// N operand reads with the wait in the same block: reads the compiler could see
+// would also wait for the copies in flight into the other stages
+__device__ __forceinline__ void lds_read2(const uint32_t (&a)[2], u32x4 (&v)[2]) {
+  asm volatile(
+      "ds_read_b128 %0, %2\n\tds_read_b128 %1, %3\n\ts_waitcnt lgkmcnt(0)"
+      : "=&v"(v[0]), "=&v"(v[1])
+      : "v"(a[0]), "v"(a[1])
+      : "memory");
+}
+__device__ __forceinline__ void lds_read4(const uint32_t (&a)[4], u32x4 (&v)[4]) {
+  asm volatile(
+      "ds_read_b128 %0, %4\n\tds_read_b128 %1, %5\n\tds_read_b128 %2, %6\n\t"
+      "ds_read_b128 %3, %7\n\ts_waitcnt lgkmcnt(0)"
+      : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3])
+      : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3])
+      : "memory");
+}
+template <int N>
+__device__ __forceinline__ void lds_read(const uint32_t (&a)[N], u32x4 (&v)[N]) {
+  if constexpr (N % 4 == 0) {
 #pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const int64_t t = t0 + 16 * j + r;
-    xp[j] = x + (t < T ? t : T - 1) * H + 8 * q;
+    for (int i = 0; i < N; i += 4) {
+      const uint32_t b[4] = {a[i], a[i + 1], a[i + 2], a[i + 3]};
+      u32x4 t[4];
+      lds_read4(b, t);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[i + k] = t[k];
+    }
+  } else if constexpr (N % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const uint32_t b[2] = {a[i], a[i + 1]};
+      u32x4 t[2];
+      lds_read2(b, t);
+      v[i] = t[0];
+      v[i + 1] = t[1];
+    }
+  } else {
+    static_assert(N == 1, "one, or an even number of reads");
+    asm volatile("ds_read_b128 %0, %1\n\ts_waitcnt lgkmcnt(0)"
+                 : "=&v"(v[0])
+                 : "v"(a[0])
+                 : "memory");
   }
+}
+
+template <int NP>
+__device__ __forceinline__ int piece_slot(int row, int p) {
+  return NP == 8 ? p ^ ((row >> 1) & 7) : p ^ (row & 15);
+}
+
+template <int TM, int TE, int KS, int WT, int WE, bool RF32, int STAGES>
+__global__ __launch_bounds__(kLgWaves * 64) void router_logits_kernel(
+    const uint16_t* __restrict__ x, const void* __restrict__ w, int T, int H, int E,
+    float* __restrict__ z) {
+  constexpr int TWN = TM / (16 * WT), EWN = TE / (16 * WE), KWN = kLgWaves / (TWN * EWN);
+  constexpr int NPX = 4 * KS, NPW = (RF32 ? 8 : 4) * KS;        // 16-byte pieces of a row
+  constexpr int kX = TM * NPX / 64, kW = TE * NPW / 64;         // copies of a stage
+  constexpr int kPer = (kX + kW) / kLgWaves;                    // a wave's
+  constexpr int kStage = (kX + kW) * 64;                        // u32x4
+  static_assert(kX % kLgWaves == 0 && kW % kLgWaves == 0 && KS % KWN == 0, "uneven waves");
+  static_assert(KWN * TM * TE * 4 <= STAGES * kStage * 16 + TM * TE * 4, "sums do not fit");
+  extern __shared__ u32x4 sl[];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, q = lane >> 4;
+  const int ew = wave % EWN, tw = wave / EWN % TWN, kw = wave / (EWN * TWN);
+  const int64_t t0 = (int64_t)blockIdx.x * TM;
+  const int e0 = blockIdx.y * TE;
+  const int ns = (H + 32 * KS - 1) / (32 * KS);
+
+  // this wave's copies: source of each at h = 0 and its piece's h; rows past the
+  // end copy the last one (their results are not stored)
+  const uint8_t* src[kPer];
+  int hof[kPer];
 #pragma unroll
-  for (int j = 0; j < ET; ++j) {
-    const int e = e0 + 4 * ET * (r >> 2) + 4 * j + (r & 3);
-    wo[j] = (int64_t)(e < E ? e : E - 1) * H + 8 * q;
+  for (int c = 0; c < kPer; ++c) {
+    const int i = wave * kPer + c;
+    // copies 0..kX-1 are x, the rest W, 64 pieces each
+    const bool is_x = i < kX;
+    const int n = (is_x ? i : i - kX) * 64 + lane, np = is_x ? NPX : NPW;
+    const int row = n / np, p = is_x ? piece_slot<NPX>(row, n % NPX) : piece_slot<NPW>(row, n % NPW);
+    if (is_x) {
+      const int64_t t = t0 + row < T ? t0 + row : T - 1;
+      src[c] = reinterpret_cast<const uint8_t*>(x + t * H);
+      hof[c] = 8 * p;
+    } else {
+      const int e = e0 + row < E ? e0 + row : E - 1;
+      src[c] = static_cast<const uint8_t*>(w) + (int64_t)e * H * (RF32 ? 4 : 2);
+      hof[c] = (RF32 ? 4 : 8) * p;
+    }
   }
-  struct Step {
-    u32x4 x[NT];
-    u32x4 w[ET][RF32 ? 2 : 1];
-  };
-  auto load = [&](Step& s, int it) {
-    const int k = 32 * (slice + (it < n_it ? it : n_it - 1) * KW);
+  auto issue = [&](int s, int buf) {
 #pragma unroll
-    for (int j = 0; j < NT; ++j) s.x[j] = *reinterpret_cast<const u32x4*>(xp[j] + k);
-#pragma unroll
-    for (int j = 0; j < ET; ++j) {
-      if (RF32) {
-        const u32x4* p =
-            reinterpret_cast<const u32x4*>(static_cast<const float*>(w) + wo[j] + k);
-        s.w[j][0] = p[0];
-        s.w[j][RF32 ? 1 : 0] = p[1];
-      } else {
-        s.w[j][0] =
-            *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(w) + wo[j] + k);
-      }
+    for (int c = 0; c < kPer; ++c) {
+      const int i = wave * kPer + c;
+      int h = 32 * KS * s + hof[c];
+      if (h >= H) h = 0;                              // not used
+      const uint8_t* g = src[c] + (int64_t)h * (RF32 && i >= kX ? 4 : 2);
+      __builtin_amdgcn_global_load_lds(g, &sl[buf * kStage + i * 64], 16, 0, 0);
     }
   };
-  v4f acc[ET][NT];
+  v4f acc[WE][WT];
 #pragma unroll
-  for (int e = 0; e < ET; ++e)
+  for (int e = 0; e < WE; ++e)
 #pragma unroll
-    for (int j = 0; j < NT; ++j) acc[e][j] = v4f{0.f, 0.f, 0.f, 0.f};
-  if (n_it > 0) {
-    Step s[D];
+    for (int j = 0; j < WT; ++j) acc[e][j] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int d = 0; d < D - 1; ++d) load(s[d], d);
-    for (int i0 = 0; i0 < n_it; i0 += D) {
+  for (int s = 0; s < STAGES - 1; ++s) issue(s < ns ? s : ns - 1, s);
+  for (int s = 0; s < ns; ++s) {
+    // this wave's copies of stage s are done once only the later STAGES - 2
+    // stages' are outstanding; the barrier shows every wave's, and that the
+    // buffer of stage s - 1 is read
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((STAGES - 2) * kPer) : "memory");
+    __builtin_amdgcn_s_barrier();
+    const int sn = s + STAGES - 1;
+    issue(sn < ns ? sn : ns - 1, sn % STAGES);
+    const u32x4* bx = &sl[(s % STAGES) * kStage];
+    const u32x4* bw = bx + kX * 64;
 #pragma unroll
-      for (int d = 0; d < D; ++d) {
-        if (i0 + d >= n_it) break;
-        load(s[(d + D - 1) % D], i0 + d + D - 1);     // past the end: the last again
+    for (int k = 0; k < KS / KWN; ++k) {
+      const int ks = k * KWN + kw;                    // the 32-h step of the stage
+      if (32 * (KS * s + ks) >= H) continue;
+      uint32_t ax[WT];
+      u32x4 vx[WT];
 #pragma unroll
-        for (int e = 0; e < ET; ++e) {
-          if (RF32) {
-            float v[8];
+      for (int j = 0; j < WT; ++j) {
+        const int row = (tw * WT + j) * 16 + r;
+        ax[j] = lds_addr(&bx[row * NPX + piece_slot<NPX>(row, 4 * ks + q)]);
+      }
+      lds_read<WT>(ax, vx);
+      constexpr int PW = RF32 ? 2 : 1;
+      uint32_t aw[WE * PW];
+      u32x4 vw[WE * PW];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(s[d].w[e][i / 4 * RF32][i % 4]);
-            u32x4 hi, mid, lo;
-            split8x3(v, hi, mid, lo);
+      for (int j = 0; j < WE; ++j) {
+        const int row = ew * WE * 16 + 4 * WE * (r >> 2) + 4 * j + (r & 3);
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-              acc[e][j] = mfma(lo, s[d].x[j], acc[e][j]);
-              acc[e][j] = mfma(mid, s[d].x[j], acc[e][j]);
-              acc[e][j] = mfma(hi, s[d].x[j], acc[e][j]);
-            }
-          } else {
+        for (int h = 0; h < PW; ++h)
+          aw[j * PW + h] = lds_addr(&bw[row * NPW + piece_slot<NPW>(row, PW * (4 * ks + q) + h)]);
+      }
+      lds_read<WE * PW>(aw, vw);
 #pragma unroll
-            for (int j = 0; j < NT; ++j) acc[e][j] = mfma(s[d].w[e][0], s[d].x[j], acc[e][j]);
+      for (int e = 0; e < WE; ++e) {
+        if (RF32) {
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(vw[e * PW + (i / 4) % PW][i % 4]);
+          u32x4 hi, mid, lo;
+          split8x3(v, hi, mid, lo);
+#pragma unroll
+          for (int j = 0; j < WT; ++j) {
+            acc[e][j] = mfma(lo, vx[j], acc[e][j]);
+            acc[e][j] = mfma(mid, vx[j], acc[e][j]);
+            acc[e][j] = mfma(hi, vx[j], acc[e][j]);
           }
+        } else {
+#pragma unroll
+          for (int j = 0; j < WT; ++j) acc[e][j] = mfma(vw[e], vx[j], acc[e][j]);
         }
       }
     }
   }
-  if (slice > 0) {
+  if constexpr (KWN > 1) {
+    // every copy has landed and every wave has read its operands: the stages
+    // become the sums' buffer
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    v4f* red = reinterpret_cast<v4f*>(sl);            // [kw - 1][tw][ew][WE * WT][64]
+    if (kw > 0) {
 #pragma unroll
-    for (int e = 0; e < ET; ++e)
+      for (int e = 0; e < WE; ++e)
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-        lred[(((slice - 1) * EW + ew) * ET * NT + e * NT + j) * 64 + lane] = acc[e][j];
+        for (int j = 0; j < WT; ++j)
+          red[((((kw - 1) * TWN + tw) * EWN + ew) * WE * WT + e * WT + j) * 64 + lane] = acc[e][j];
+    }
+    __syncthreads();
+    if (kw > 0) return;
+#pragma unroll
+    for (int k = 0; k < KWN - 1; ++k)
+#pragma unroll
+      for (int e = 0; e < WE; ++e)
+#pragma unroll
+        for (int j = 0; j < WT; ++j)
+          acc[e][j] += red[(((k * TWN + tw) * EWN + ew) * WE * WT + e * WT + j) * 64 + lane];
   }
-  __syncthreads();
-  if (slice > 0) return;
-  for (int k = 0; k < KW - 1; ++k)
 #pragma unroll
-    for (int e = 0; e < ET; ++e)
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-        acc[e][j] += lred[((k * EW + ew) * ET * NT + e * NT + j) * 64 + lane];
-#pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const int64_t t = t0 + 16 * j + r;
+  for (int j = 0; j < WT; ++j) {
+    const int64_t t = t0 + (tw * WT + j) * 16 + r;
     if (t >= T) continue;
 #pragma unroll
-    for (int e = 0; e < ET; ++e) {
-      const int c = e0 + 4 * ET * q + 4 * e;
+    for (int e = 0; e < WE; ++e) {
+      const int c = e0 + ew * WE * 16 + 4 * WE * q + 4 * e;
       float* o = z + t * E + c;
       if (E % 4 == 0) {
         if (c < E) *reinterpret_cast<v4f*>(o) = acc[e][j];
@@ -176,14 +273,13 @@ __global__ __launch_bounds__(kLgWaves * 64, 2) void router_logits_kernel(
   }
 }
 
-template <int NT, int ET, bool RF32, int D>
-hipError_t run_logits(const void* x, const void* w, int T, int H, int E, int log_ew, float* z,
+template <int TM, int TE, int KS, int WT, int WE, bool RF32, int STAGES>
+hipError_t run_logits(const void* x, const void* w, int T, int H, int E, float* z,
                       hipStream_t st) {
-  const int ew = 1 << log_ew;
-  const dim3 g((T + 16 * NT - 1) / (16 * NT), (E + 16 * ET * ew - 1) / (16 * ET * ew));
-  const size_t lds = (size_t)(kLgWaves - ew) * ET * NT * 64 * sizeof(v4f);
-  hipLaunchKernelGGL((router_logits_kernel<NT, ET, RF32, D>), g, dim3(kLgWaves * 64), lds, st,
-                     static_cast<const uint16_t*>(x), w, T, H, E, log_ew, z);
+  const dim3 g((T + TM - 1) / TM, (E + TE - 1) / TE);
+  constexpr size_t lds = (size_t)STAGES * (TM * 4 + TE * (RF32 ? 8 : 4)) * KS * 16;
+  hipLaunchKernelGGL((router_logits_kernel<TM, TE, KS, WT, WE, RF32, STAGES>), g,
+                     dim3(kLgWaves * 64), lds, st, static_cast<const uint16_t*>(x), w, T, H, E, z);
   return hipGetLastError();
 }
 
@@ -502,22 +598,20 @@ hipError_t launch_router_logits(const void* x, const void* w, int router_f32, in
                                 float* z, hipStream_t st) {
   // The widest tile that still gives 192 workgroups (3/4 of the compute units):
   // 64 tokens x 256 experts reads x once and W for every 64 tokens; then fewer
-  // experts (more slices of H per workgroup), fewer tokens, last 16 x 16.
+  // experts; last 16 x 32, where a workgroup's waves all split H.
   const auto blocks = [&](int tokens, int experts) {
     return (int64_t)((T + tokens - 1) / tokens) * ((E + experts - 1) / experts);
   };
-  for (int log_ew = E > 128 ? 2 : E > 64 ? 1 : 0; log_ew >= 0; --log_ew)
-    if (blocks(64, 64 << log_ew) >= 192)
-      return router_f32 ? run_logits<4, 4, true, 2>(x, w, T, H, E, log_ew, z, st)
-                        : run_logits<4, 4, false, 3>(x, w, T, H, E, log_ew, z, st);
-  if (blocks(32, 64) >= 192)
-    return router_f32 ? run_logits<2, 4, true, 2>(x, w, T, H, E, 0, z, st)
-                      : run_logits<2, 4, false, 3>(x, w, T, H, E, 0, z, st);
-  if (blocks(16, 64) >= 192)
-    return router_f32 ? run_logits<1, 4, true, 2>(x, w, T, H, E, 0, z, st)
-                      : run_logits<1, 4, false, 3>(x, w, T, H, E, 0, z, st);
-  return router_f32 ? run_logits<1, 1, true, 4>(x, w, T, H, E, 0, z, st)
-                    : run_logits<1, 1, false, 4>(x, w, T, H, E, 0, z, st);
+  if (router_f32) {
+    if (E > 128 && blocks(64, 256) >= 192) return run_logits<64, 256, 2, 4, 4, true, 2>(x, w, T, H, E, z, st);
+    if (E > 64 && blocks(64, 128) >= 192) return run_logits<64, 128, 2, 2, 4, true, 3>(x, w, T, H, E, z, st);
+    if (blocks(64, 64) >= 192) return run_logits<64, 64, 2, 1, 4, true, 4>(x, w, T, H, E, z, st);
+    return run_logits<16, 32, 8, 1, 2, true, 3>(x, w, T, H, E, z, st);
+  }
+  if (E > 128 && blocks(64, 256) >= 192) return run_logits<64, 256, 2, 4, 4, false, 3>(x, w, T, H, E, z, st);
+  if (E > 64 && blocks(64, 128) >= 192) return run_logits<64, 128, 2, 2, 4, false, 4>(x, w, T, H, E, z, st);
+  if (blocks(64, 64) >= 192) return run_logits<64, 64, 2, 1, 4, false, 4>(x, w, T, H, E, z, st);
+  return run_logits<16, 32, 8, 1, 2, false, 4>(x, w, T, H, E, z, st);
 }
 
 size_t router_backward_bytes(int T, int H, int E) { return carve(T, H, E).total; }

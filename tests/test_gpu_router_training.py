@@ -203,6 +203,8 @@ ROUTER = [
     (777, 2048, 128, "f32"), (515, 288, 130, "bf16"), (129, 512, 300, "bf16"),
     (300, 160, 1000, "f32"), (4100, 320, 256, "bf16"), (64, 4096, 256, "bf16"),
     (2048, 64, 20, "bf16"),
+    (12289, 96, 200, "bf16"), (12289, 160, 256, "f32"), (12300, 64, 100, "f32"),
+    (12300, 96, 101, "bf16"), (12300, 32, 40, "f32"), (12300, 224, 64, "bf16"),
 ]
 
 
