@@ -325,30 +325,43 @@ __global__ __launch_bounds__(kDxWaves * 64) void router_dx_kernel(const float* _
   const int nks = (E + 31) / 32, nc = (H + 63) / 64;
   const int64_t t0 = (int64_t)blockIdx.x * 16 * NTL;
   const bool vec = E % 4 == 0;
-  for (int it = wave; it < nks * NTL; it += kDxWaves) {
-    const int ks = it / NTL, nt = it % NTL;
-    const int64_t t = t0 + 16 * nt + n;
-    const int e0 = 32 * ks + 8 * q;
-    float v[8] = {};
-    if (t < T) {
-      const float* src = dz + t * E + e0;
-      if (vec) {
+  // four pieces' loads in flight before the first is used
+  for (int i0 = wave; i0 < nks * NTL; i0 += 4 * kDxWaves) {
+    float v[4][8];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (e0 + 4 * i < E) {
-            const float4 f = *reinterpret_cast<const float4*>(src + 4 * i);
-            v[4 * i] = f.x; v[4 * i + 1] = f.y; v[4 * i + 2] = f.z; v[4 * i + 3] = f.w;
-          }
-      } else {
+    for (int u = 0; u < 4; ++u) {
+      const int it = i0 + u * kDxWaves, ks = it / NTL, nt = it % NTL;
+      const int64_t t = t0 + 16 * nt + n;
+      const int e0 = 32 * ks + 8 * q;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (e0 + i < E) v[i] = src[i];
+      for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
+      if (it < nks * NTL && t < T) {
+        const float* src = dz + t * E + e0;
+        if (vec) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (e0 + 4 * i < E) {
+              const float4 f = *reinterpret_cast<const float4*>(src + 4 * i);
+              v[u][4 * i] = f.x; v[u][4 * i + 1] = f.y;
+              v[u][4 * i + 2] = f.z; v[u][4 * i + 3] = f.w;
+            }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (e0 + i < E) v[u][i] = src[i];
+        }
       }
     }
-    u32x4 hi, lo;
-    split8(v, hi, lo);
-    sb[(it * 2) * 64 + lane] = hi;
-    sb[(it * 2 + 1) * 64 + lane] = lo;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int it = i0 + u * kDxWaves;
+      if (it < nks * NTL) {
+        u32x4 hi, lo;
+        split8(v[u], hi, lo);
+        sb[(it * 2) * 64 + lane] = hi;
+        sb[(it * 2 + 1) * 64 + lane] = lo;
+      }
+    }
   }
   __syncthreads();
   for (int c = blockIdx.y * kDxWaves + wave; c < nc; c += gridDim.y * kDxWaves) {
@@ -371,11 +384,12 @@ __global__ __launch_bounds__(kDxWaves * 64) void router_dx_kernel(const float* _
         const u32x4 hi = sb[((ks * NTL + t) * 2) * 64 + lane];
         const u32x4 lo = sb[((ks * NTL + t) * 2 + 1) * 64 + lane];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          acc[j][t] = mfma(a[j * PL], hi, acc[j][t]);
-          acc[j][t] = mfma(a[j * PL], lo, acc[j][t]);
-          if (RF32) acc[j][t] = mfma(a[j * PL + PL - 1], hi, acc[j][t]);
-        }
+        for (int j = 0; j < 4; ++j) acc[j][t] = mfma(a[j * PL], lo, acc[j][t]);
+        if (RF32)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[j][t] = mfma(a[j * PL + PL - 1], hi, acc[j][t]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[j][t] = mfma(a[j * PL], hi, acc[j][t]);
       }
 #pragma unroll
       for (int i = 0; i < 4 * PL; ++i) a[i] = an[i];
@@ -428,12 +442,12 @@ __global__ __launch_bounds__(256) void pack_dz_kernel(const float* __restrict__ 
 }
 
 // ---- dW -----------------------------------------------------------------------
-// A workgroup: 16 ET experts x 256 h over a slice of the tokens.  dz^T of 32
-// tokens goes through LDS (double buffered), shared by the four waves; a wave
+// A workgroup: 16 ET experts x 512 h over a slice of the tokens.  dz^T of 32
+// tokens goes through LDS (double buffered), shared by the eight waves; a wave
 // has 64 h of its own, whose x it reads straight from memory (lane (n, q): 8
 // tokens x 4 h) and transposes in registers: column n of the f-th operand is
 // h = 4 n + f, so a lane ends up with four consecutive h of a row.
-constexpr int kDwWaves = 4;
+constexpr int kDwWaves = 8, kDwH = 64 * kDwWaves;
 
 __device__ __forceinline__ uint32_t pack_lo(uint32_t a, uint32_t b) {
   return __builtin_amdgcn_perm(b, a, 0x05040100u);
@@ -451,7 +465,7 @@ __global__ __launch_bounds__(kDwWaves * 64, 2) void router_dw_kernel(
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, q = lane >> 4;
   const int nkt = (T + 31) / 32;
   const int k0 = blockIdx.z * per_slice, k1 = min(nkt, k0 + per_slice);
-  const int h = blockIdx.x * 256 + wave * 64 + 4 * n;
+  const int h = blockIdx.x * kDwH + wave * 64 + 4 * n;
   const bool hin = h < H;
   const u32x4* zsrc = zf + (int64_t)blockIdx.y * ET * kZp * 64;
 
@@ -534,20 +548,20 @@ __global__ __launch_bounds__(256) void sum_slices_kernel(const v4f* __restrict__
 }
 
 // experts per dW workgroup in tiles of 16, the number of those tiles, and the
-// token slices: two workgroups per compute unit where a slice has at least 8
+// token slices: a workgroup per compute unit where a slice has at least 8
 // steps of 32 tokens; short batches take fewer experts a workgroup instead
 struct DwPlan {
   int et, net, slices, per_slice;
 };
 DwPlan dw_plan(int T, int H, int E) {
   DwPlan p;
-  const int nkt = T > 0 ? (T + 31) / 32 : 1, hx = (H + 255) / 256;
+  const int nkt = T > 0 ? (T + 31) / 32 : 1, hx = (H + kDwH - 1) / kDwH;
   const int most = nkt / 8 > 1 ? nkt / 8 : 1;
   p.et = E > 64 ? 8 : E > 32 ? 4 : E > 16 ? 2 : 1;
   while (p.et > 1 && hx * ((E + 16 * p.et - 1) / (16 * p.et)) * most < 192) p.et /= 2;
   const int ey = (E + 16 * p.et - 1) / (16 * p.et), tiles = ey * hx;
   p.net = ey * p.et;
-  int s = (512 + tiles - 1) / tiles;
+  int s = (256 + tiles - 1) / tiles;
   if (s > most) s = most;
   p.per_slice = (nkt + s - 1) / s;
   p.slices = (nkt + p.per_slice - 1) / p.per_slice;
@@ -596,19 +610,21 @@ hipError_t run_dx(const RouterBackward& a, const u32x4* wf, hipStream_t st) {
 
 hipError_t launch_router_logits(const void* x, const void* w, int router_f32, int T, int H, int E,
                                 float* z, hipStream_t st) {
-  // The widest tile that still gives 192 workgroups (3/4 of the compute units):
-  // 64 tokens x 256 experts reads x once and W for every 64 tokens; then fewer
-  // experts; last 16 x 32, where a workgroup's waves all split H.
+  // A compute unit takes in about 40 GB/s through its L1 here (its misses in
+  // flight over the L2's latency), so the tile with the fewest bytes per result
+  // that still gives 192 workgroups (3/4 of the compute units) is the fastest:
+  // 128 x 128 before 64 x 128 before 64 x 64; last 16 x 32, where a workgroup's
+  // waves all split H.  T = 16384, H = 4096, E = 256: 64 x 256 tiles 63 us.
   const auto blocks = [&](int tokens, int experts) {
     return (int64_t)((T + tokens - 1) / tokens) * ((E + experts - 1) / experts);
   };
   if (router_f32) {
-    if (E > 128 && blocks(64, 256) >= 192) return run_logits<64, 256, 2, 4, 4, true, 2>(x, w, T, H, E, z, st);
+    if (E > 64 && blocks(128, 128) >= 192) return run_logits<128, 128, 2, 4, 4, true, 3>(x, w, T, H, E, z, st);
     if (E > 64 && blocks(64, 128) >= 192) return run_logits<64, 128, 2, 2, 4, true, 3>(x, w, T, H, E, z, st);
     if (blocks(64, 64) >= 192) return run_logits<64, 64, 2, 1, 4, true, 4>(x, w, T, H, E, z, st);
     return run_logits<16, 32, 8, 1, 2, true, 3>(x, w, T, H, E, z, st);
   }
-  if (E > 128 && blocks(64, 256) >= 192) return run_logits<64, 256, 2, 4, 4, false, 3>(x, w, T, H, E, z, st);
+  if (E > 64 && blocks(128, 128) >= 192) return run_logits<128, 128, 2, 4, 4, false, 4>(x, w, T, H, E, z, st);
   if (E > 64 && blocks(64, 128) >= 192) return run_logits<64, 128, 2, 2, 4, false, 4>(x, w, T, H, E, z, st);
   if (blocks(64, 64) >= 192) return run_logits<64, 64, 2, 1, 4, false, 4>(x, w, T, H, E, z, st);
   return run_logits<16, 32, 8, 1, 2, false, 4>(x, w, T, H, E, z, st);
@@ -639,7 +655,7 @@ hipError_t launch_router_backward(const RouterBackward& a, hipStream_t st) {
   err = hipGetLastError();
   if (err != hipSuccess) return err;
   float* out = p.slices > 1 ? reinterpret_cast<float*>(a.ws + L.part) : a.dw;
-  const dim3 g((a.H + 255) / 256, p.net / p.et, p.slices), b(kDwWaves * 64);
+  const dim3 g((a.H + kDwH - 1) / kDwH, p.net / p.et, p.slices), b(kDwWaves * 64);
   const uint16_t* x = static_cast<const uint16_t*>(a.x);
   if (p.et == 8)
     hipLaunchKernelGGL(router_dw_kernel<8>, g, b, 0, st, x, zf, a.T, a.H, a.E, p.net, p.per_slice,
