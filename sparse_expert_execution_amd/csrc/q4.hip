@@ -43,11 +43,12 @@ q4_linear_kernel(Q4Linear a) {
     Tile<G, ZERO> t[RT];
     bf16x8 x[NT][4];
   };
+  const int n_it = (a.nkb - slice + KS - 1) >> a.log_ks;
   auto load = [&](Block& b, int it) {
-    const int last = (a.nkb - 1 - slice) >> a.log_ks;   // >= 0: KS <= nkb
-    const int kb = slice + ((it < last ? it : last) << a.log_ks);
+    const bool live = it < n_it;                      // n_it >= 1: KS <= nkb
+    const int kb = slice + ((live ? it : 0) << a.log_ks);
 #pragma unroll
-    for (int r = 0; r < RT; ++r) load_tile<G, ZERO>(b.t[r], m, tile[r], kb);
+    for (int r = 0; r < RT; ++r) load_tile<G, ZERO>(b.t[r], m, tile[r], kb, live);
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const int t = t0 + 16 * j + slot_token(lane & 15);
@@ -57,8 +58,8 @@ q4_linear_kernel(Q4Linear a) {
         const int k = 128 * kb + 32 * s + 8 * q;
         u32x4 v = u32x4{0, 0, 0, 0};
         if (VEC) {
-          if (t < a.T && k < a.K) v = *reinterpret_cast<const u32x4*>(row + k);
-        } else if (t < a.T) {
+          if (live && t < a.T && k < a.K) v = *reinterpret_cast<const u32x4*>(row + k);
+        } else if (live && t < a.T) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             if (k + i < a.K) v[i / 2] |= (uint32_t)row[k + i] << (16 * (i % 2));
@@ -68,7 +69,6 @@ q4_linear_kernel(Q4Linear a) {
     }
   };
 
-  const int n_it = (a.nkb - slice + KS - 1) >> a.log_ks;
   Block b[D];
 #pragma unroll
   for (int d = 0; d < D - 1; ++d) load(b[d], d);
@@ -76,7 +76,7 @@ q4_linear_kernel(Q4Linear a) {
 #pragma unroll
     for (int d = 0; d < D; ++d) {
       if (i0 + d >= n_it) break;
-      load(b[(d + D - 1) % D], i0 + d + D - 1);       // past the end: the last again
+      load(b[(d + D - 1) % D], i0 + d + D - 1);
       mul_tiles<RT, NT, TI, G, ZERO>(acc, b[d].t, b[d].x);
     }
   }

@@ -73,9 +73,12 @@ struct Matrix {
   int nkb;                  // column blocks of 128
 };
 
+// live = false (the same for the whole wave): a step past the end, whose loads
+// stay so that the waits keep their counts, all lanes on one line
 template <int G, bool ZERO>
-__device__ __forceinline__ void load_tile(Tile<G, ZERO>& t, const Matrix& m, int tile, int kb) {
-  const int lane = threadIdx.x & 63;
+__device__ __forceinline__ void load_tile(Tile<G, ZERO>& t, const Matrix& m, int tile, int kb,
+                                          bool live) {
+  const int lane = live ? threadIdx.x & 63 : 0;
   const int64_t at = (int64_t)tile * m.nkb + kb;
   t.codes = ldg16(m.codes + (at * 64 + lane) * 16);
   const int64_t gi = at * (128 / G) * 16 + (lane & 15);

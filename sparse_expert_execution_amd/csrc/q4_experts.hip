@@ -6,9 +6,8 @@
 //
 // Bound: HBM, the bytes of the distinct experts.  The unit of work is a
 // distinct expert with the pairs that chose it (the shared expert: all
-// tokens).  A first launch makes the list of units, so that the workgroups of
-// the two product kernels find theirs with one load, however many pairs name
-// the same expert.
+// tokens).  Up to 64 pairs every workgroup lists the units itself, with one
+// wave; more pairs take a launch of their own for the list.
 #include "q4.hpp"
 
 namespace moe {
@@ -69,6 +68,45 @@ __global__ __launch_bounds__(kUnitThreads) void q4_units_kernel(Q4Experts a) {
   if (i == 0) *a.n_units = routed + (a.shared ? 1 : 0);
 }
 
+// The same list of at most 64 pairs by one wave, into LDS.  Lane i is pair i.
+constexpr int kWavePairs = 64;
+
+struct UnitList {
+  int4 unit[kWavePairs + 1];
+  int16_t entry[kWavePairs + kQ4MaxTokens];
+  int n;
+};
+
+__device__ __forceinline__ void wave_units(const Q4Experts& a, UnitList& u) {
+  const int i = threadIdx.x & 63;
+  int id = -1, slot = -1;
+  if (i < a.P) {
+    id = a.ids[i];
+    if (id >= 0 && id < a.E) slot = a.slot_of ? a.slot_of[id] : id;
+    if (slot < 0) id = -1;
+  }
+  int first = 64, rank = 0, count = 0;
+  for (int j = 0; j < a.P; ++j) {
+    const bool same = __builtin_amdgcn_readlane(id, j) == id;
+    first = same && j < first ? j : first;
+    rank += same && j < i;
+    count += same;
+  }
+  const bool lead = id >= 0 && first == i;
+  const int packed = lead ? 1 << 16 | count : 0;
+  const int inc = wave_scan_dpp(packed), before = inc - packed;
+  const int total = __builtin_amdgcn_readlane(inc, 63);
+  const int base = __shfl(before & 0xffff, first & 63, kWave);
+  if (lead) u.unit[before >> 16] = make_int4(slot, before & 0xffff, count, 0);
+  if (id >= 0) u.entry[base + rank] = (int16_t)i;
+  const int routed = total >> 16, pairs = total & 0xffff;
+  if (a.shared) {
+    if (i == 0) u.unit[routed] = make_int4(-1, pairs, a.T, 0);
+    if (i < a.T) u.entry[pairs + i] = (int16_t)(a.P + i);
+  }
+  if (i == 0) u.n = routed + (a.shared ? 1 : 0);
+}
+
 // ---- gate / up --------------------------------------------------------------
 // grid (row tiles of I, units).  A workgroup's waves are KS slices of H for one
 // row tile of both matrices; the partial sums meet in LDS in slice order.
@@ -97,13 +135,14 @@ __device__ __forceinline__ void gate_up_columns(const Q4Experts& a, const uint8_
   };
   const int n_it = wave < nkb ? (nkb - wave + kGuWaves - 1) / kGuWaves : 0;
   auto load = [&](Block& b, int it) {
-    const int kb = wave + (it < n_it ? it : n_it - 1) * kGuWaves;
-    load_tile<G, false>(b.t[0], mg, tile, kb);
-    load_tile<G, false>(b.t[1], mu, tile, kb);
+    const bool in = it < n_it;
+    const int kb = wave + (in ? it : 0) * kGuWaves;
+    load_tile<G, false>(b.t[0], mg, tile, kb, in);
+    load_tile<G, false>(b.t[1], mu, tile, kb, in);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       u32x4 v = u32x4{0, 0, 0, 0};
-      if (live && 128 * kb + 32 * s + 8 * q < a.H)
+      if (in && live && 128 * kb + 32 * s + 8 * q < a.H)
         v = *reinterpret_cast<const u32x4*>(xrow + 128 * kb + 32 * s);
       b.x[0][s] = frag(v);
     }
@@ -119,7 +158,7 @@ __device__ __forceinline__ void gate_up_columns(const Q4Experts& a, const uint8_
 #pragma unroll
       for (int d = 0; d < D; ++d) {
         if (i0 + d >= n_it) break;
-        load(b[(d + D - 1) % D], i0 + d + D - 1);     // past the end: the last again
+        load(b[(d + D - 1) % D], i0 + d + D - 1);
         mul_tiles<2, 1, TI, G, false>(acc, b[d].t, b[d].x);
       }
     }
@@ -156,15 +195,28 @@ __device__ __forceinline__ void gate_up_columns(const Q4Experts& a, const uint8_
   }
 }
 
-template <int G>
+template <int G, bool SMALL>
 __global__ __launch_bounds__(kGuWaves * 64, 4) void q4_gate_up_kernel(Q4Experts a) {
   __shared__ float red[2][4][kGuWaves][64];
-  if ((int)blockIdx.y >= *a.n_units) return;
-  const int4 u = a.units[blockIdx.y];
-  const uint8_t* block = u.x < 0 ? a.shared : a.pool + (int64_t)u.x * a.expert_bytes;
-  const int16_t* entries = a.entries + u.y;
-  for (int c0 = 0; c0 < u.z; c0 += 16) {
-    const int n = min(16, u.z - c0);
+  __shared__ UnitList list;
+  int4 u;
+  const int16_t* entries;
+  if (SMALL) {
+    if (threadIdx.x < 64) wave_units(a, list);
+    __syncthreads();
+    if ((int)blockIdx.y >= list.n) return;
+    u = list.unit[blockIdx.y];
+    entries = list.entry + u.y;
+  } else {
+    if ((int)blockIdx.y >= *a.n_units) return;
+    u = a.units[blockIdx.y];
+    entries = a.entries + u.y;
+  }
+  const int slot = __builtin_amdgcn_readfirstlane(u.x);
+  const int count = __builtin_amdgcn_readfirstlane(u.z);
+  const uint8_t* block = slot < 0 ? a.shared : a.pool + (int64_t)slot * a.expert_bytes;
+  for (int c0 = 0; c0 < count; c0 += 16) {
+    const int n = min(16, count - c0);
     if (n <= 4) gate_up_columns<1, G>(a, block, blockIdx.x, entries + c0, n, red);
     else if (n <= 8) gate_up_columns<2, G>(a, block, blockIdx.x, entries + c0, n, red);
     else gate_up_columns<4, G>(a, block, blockIdx.x, entries + c0, n, red);
@@ -183,74 +235,134 @@ __global__ __launch_bounds__(kGuWaves * 64, 4) void q4_gate_up_kernel(Q4Experts 
 // columns, and a lane's result i is entry i of part l / 16.
 constexpr int kDnWaves = 16;
 
-template <int G>
+template <int G, bool SMALL>
 __global__ __launch_bounds__(kDnWaves * 64, 4) void q4_down_kernel(Q4Experts a, int cut) {
-  constexpr int D = 2;
+  constexpr int D = 3;
+  constexpr int kPairs = SMALL ? kWavePairs : kQ4MaxPairs;
   extern __shared__ float yl[];                       // [wave][T][16]
-  __shared__ int4 s_unit[kQ4MaxPairs + 1];
+  __shared__ UnitList list;
+  __shared__ int4 s_unit[SMALL ? 1 : kPairs + 1];
+  __shared__ int16_t s_entry[SMALL ? 1 : kPairs + kQ4MaxTokens];
+  __shared__ float s_w[kPairs + kQ4MaxTokens];
+  __shared__ uint8_t s_token[kPairs + kQ4MaxTokens];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 4, n = lane & 15;
-  const int n_units = *a.n_units;
-  for (int i = threadIdx.x; i < n_units; i += kDnWaves * 64) s_unit[i] = a.units[i];
+  // by pair: the token and the gate weight
+  for (int i = threadIdx.x; i < a.P + a.T; i += kDnWaves * 64) {
+    s_token[i] = (uint8_t)(i < a.P ? i / a.k : i - a.P);
+    s_w[i] = i < a.P ? a.w[i] : 1.f;
+  }
   for (int j = threadIdx.x; j < kDnWaves * a.T * 16; j += kDnWaves * 64) yl[j] = 0.f;
-  __syncthreads();
+  int n_units;
+  const int4* units;
+  const int16_t* entries;
+  if (SMALL) {
+    if (threadIdx.x < 64) wave_units(a, list);
+    __syncthreads();
+    n_units = list.n;
+    units = list.unit;
+    entries = list.entry;
+  } else {
+    n_units = *a.n_units;
+    for (int i = threadIdx.x; i < n_units; i += kDnWaves * 64) s_unit[i] = a.units[i];
+    for (int i = threadIdx.x; i < a.P + a.T; i += kDnWaves * 64) s_entry[i] = a.entries[i];
+    __syncthreads();
+    units = s_unit;
+    entries = s_entry;
+  }
+  n_units = __builtin_amdgcn_readfirstlane(n_units);
   const int nkb = (a.I + 127) / 128, tile = blockIdx.x;
   const int per = (nkb + cut - 1) / cut;              // column blocks of a job
-  const int slices = (nkb + per - 1) / per;
+  const int slices = (nkb + per - 1) / per, jobs = n_units * slices;
   const int64_t plane = (int64_t)(a.P + a.T) * a.I;
   float* mine = yl + (int64_t)wave * a.T * 16;
   const int part = n >> 2, e4 = n & 3;                // as an operand row
 
+  // where the loads are: a job, four of its entries, a column block
+  int job = __builtin_amdgcn_readfirstlane(wave), c0 = 0, kb = 0, kend = 0, first = 0, count = 0;
+  Matrix m{nullptr, nullptr, nullptr, nkb};
+  const uint16_t* hrow = nullptr;
+  bool live = false;
+  auto chunk = [&]() {
+    live = part < 3 && c0 + e4 < count;
+    hrow = a.h + 8 * q;
+    if (live) hrow += part * plane + (int64_t)entries[first + c0 + e4] * a.I;
+  };
+  int k0 = 0;
+  auto start = [&]() {
+    const int ui = job / slices;
+    k0 = (job - ui * slices) * per;
+    kend = min(k0 + per, nkb);
+    kb = k0;
+    c0 = 0;
+    const int4 u = units[ui];
+    const int slot = __builtin_amdgcn_readfirstlane(u.x);
+    first = __builtin_amdgcn_readfirstlane(u.y);
+    count = __builtin_amdgcn_readfirstlane(u.z);
+    const uint8_t* block = slot < 0 ? a.shared : a.pool + (int64_t)slot * a.expert_bytes;
+    m.codes = block + a.off[4];
+    m.scales = block + a.off[5];
+    chunk();
+  };
+
+  // a column block in flight; at the last one of a chunk: its entries' number
   struct Block {
     Tile<G, false> t[1];
     bf16x8 x[1][4];
+    int valid, flush, at;
   };
-  for (int job = wave; job < n_units * slices; job += kDnWaves) {
-    const int ui = __builtin_amdgcn_readfirstlane(job / slices);
-    const int k0 = (job - ui * slices) * per, n_it = min(per, nkb - k0);
-    const int4 u = s_unit[ui];
-    const int slot = __builtin_amdgcn_readfirstlane(u.x);
-    const uint8_t* block = slot < 0 ? a.shared : a.pool + (int64_t)slot * a.expert_bytes;
-    const Matrix m{block + a.off[4], block + a.off[5], nullptr, nkb};
-    const int count = __builtin_amdgcn_readfirstlane(u.z);
-    const int16_t* entries = a.entries + __builtin_amdgcn_readfirstlane(u.y);
-    for (int c0 = 0; c0 < count; c0 += 4) {           // past the first: the tile from cache
-      const int nc = min(4, count - c0);
-      const bool live = part < 3 && e4 < nc;
-      const uint16_t* hrow = a.h + 8 * q;
-      if (live) hrow += part * plane + (int64_t)entries[c0 + e4] * a.I;
-      auto load = [&](Block& b, int it) {
-        const int kb = k0 + (it < n_it ? it : n_it - 1);
-        load_tile<G, false>(b.t[0], m, tile, kb);
+  auto load = [&](Block& b) {
+    const bool in = job < jobs;
+    b.valid = in;
+    load_tile<G, false>(b.t[0], m, tile, kb, in);
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          u32x4 v = u32x4{0, 0, 0, 0};
-          if (live && 128 * kb + 32 * s + 8 * q < a.I)
-            v = *reinterpret_cast<const u32x4*>(hrow + 128 * kb + 32 * s);
-          b.x[0][s] = frag(v);
-        }
-      };
-      float acc[1][1][4] = {};
-      Block b[D];
-#pragma unroll
-      for (int d = 0; d < D - 1; ++d) load(b[d], d);
-      for (int i0 = 0; i0 < n_it; i0 += D) {
-#pragma unroll
-        for (int d = 0; d < D; ++d) {
-          if (i0 + d >= n_it) break;
-          load(b[(d + D - 1) % D], i0 + d + D - 1);
-          mul_tiles<1, 1, 4, G, false>(acc, b[d].t, b[d].x);
-        }
+    for (int s = 0; s < 4; ++s) {
+      u32x4 v = u32x4{0, 0, 0, 0};
+      if (in && live && 128 * kb + 32 * s + 8 * q < a.I)
+        v = *reinterpret_cast<const u32x4*>(hrow + 128 * kb + 32 * s);
+      b.x[0][s] = frag(v);
+    }
+    b.flush = 0;
+    b.at = first + c0;
+    if (!in) return;
+    if (++kb == kend) {
+      b.flush = min(4, count - c0);
+      c0 += 4;
+      kb = k0;
+      if (c0 < count) {
+        chunk();                                      // the tile again, from cache
+      } else {
+        job += kDnWaves;
+        if (job < jobs) start();
       }
+    }
+  };
+  if (job < jobs) {
+    start();
+    Block b[D];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (i >= nc) break;
-        // small parts first; lanes 0..15 hold the sum of the three
-        const float v = acc[0][0][i] +
-                        (__shfl(acc[0][0][i], n + 16, kWave) + __shfl(acc[0][0][i], n + 32, kWave));
-        if (q == 0) {
-          const int e = entries[c0 + i];
-          const float w = e < a.P ? a.w[e] : 1.f;
-          mine[(e < a.P ? e / a.k : e - a.P) * 16 + n] += w * v;
+    for (int d = 0; d < D - 1; ++d) load(b[d]);
+    float acc[1][1][4] = {};
+    for (bool more = true; more;) {
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        if (!b[d].valid) {
+          more = false;
+          break;
+        }
+        load(b[(d + D - 1) % D]);
+        mul_tiles<1, 1, 4, G, false>(acc, b[d].t, b[d].x);
+        if (b[d].flush == 0) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          // small parts first; lanes 0..15 hold the sum of the three
+          const float v =
+              acc[0][0][i] + (__shfl(acc[0][0][i], n + 16, kWave) +
+                              __shfl(acc[0][0][i], n + 32, kWave));
+          acc[0][0][i] = 0.f;
+          if (q == 0 && i < b[d].flush) {
+            const int e = entries[b[d].at + i];
+            mine[s_token[e] * 16 + n] += s_w[e] * v;
+          }
         }
       }
     }
@@ -264,22 +376,28 @@ __global__ __launch_bounds__(kDnWaves * 64, 4) void q4_down_kernel(Q4Experts a, 
   }
 }
 
-template <int G>
-hipError_t run(const Q4Experts& a, hipStream_t st) {
-  hipLaunchKernelGGL(q4_units_kernel, dim3(1), dim3(kUnitThreads), 0, st, a);
-  hipError_t err = hipGetLastError();
-  if (err != hipSuccess) return err;
+template <int G, bool SMALL>
+hipError_t run_products(const Q4Experts& a, hipStream_t st) {
   const int most = (a.P < a.E ? a.P : a.E) + (a.shared ? 1 : 0);   // units at most
-  hipLaunchKernelGGL((q4_gate_up_kernel<G>), dim3(a.I / 16, most), dim3(kGuWaves * 64), 0, st, a);
-  err = hipGetLastError();
+  hipLaunchKernelGGL((q4_gate_up_kernel<G, SMALL>), dim3(a.I / 16, most), dim3(kGuWaves * 64), 0,
+                     st, a);
+  const hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   // enough jobs for four rounds of the waves: an uneven last one costs little
   int cut = (4 * kDnWaves + most - 1) / most;
   const int nkb = (a.I + 127) / 128;
   cut = cut < 1 ? 1 : cut > nkb ? nkb : cut;
-  hipLaunchKernelGGL((q4_down_kernel<G>), dim3(a.H / 16), dim3(kDnWaves * 64),
+  hipLaunchKernelGGL((q4_down_kernel<G, SMALL>), dim3(a.H / 16), dim3(kDnWaves * 64),
                      (size_t)kDnWaves * a.T * 16 * sizeof(float), st, a, cut);
   return hipGetLastError();
+}
+
+template <int G>
+hipError_t run(const Q4Experts& a, hipStream_t st) {
+  if (a.P <= kWavePairs) return run_products<G, true>(a, st);
+  hipLaunchKernelGGL(q4_units_kernel, dim3(1), dim3(kUnitThreads), 0, st, a);
+  const hipError_t err = hipGetLastError();
+  return err != hipSuccess ? err : run_products<G, false>(a, st);
 }
 
 }  // namespace
