@@ -202,6 +202,11 @@ static int q4_decode_impl(const moe_desc* desc, const void* x, const void* w_rou
                           int32_t* ids, float* w, const int32_t* slot_of_expert,
                           const void* slot_pool, const void* shared_expert, float* y, void* ws,
                           size_t ws_bytes, void* stream) {
+  // the kernels address the rows of x and h by 32-bit byte offsets
+  if ((int64_t)T * desc->hidden * 2 >= (int64_t)1 << 31 ||
+      (int64_t)T * (desc->top_k + 1) * desc->inter * 6 >= (int64_t)1 << 31)
+    return set_error(MOE_EUNSUPPORTED, "decode shape H=%d I=%d too wide for %d tokens",
+                     desc->hidden, desc->inter, T);
   const Q4DecodeWs L = q4_decode_ws(desc, T);
   if (!ws || ws_bytes < L.total || !aligned(ws, 256))
     return set_error(MOE_EWORKSPACE, "decode workspace %zu < %zu bytes (or not 256-aligned)",

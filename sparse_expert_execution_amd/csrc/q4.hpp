@@ -73,19 +73,38 @@ struct Matrix {
   int nkb;                  // column blocks of 128
 };
 
-// live = false (the same for the whole wave): a step past the end, whose loads
-// stay so that the waits keep their counts, all lanes on one line
+// tile, kb and live are the same for the whole wave, so the addresses are a
+// scalar base and a lane's constant offset.  live = false: a step past the end,
+// whose loads stay so that the waits keep their counts, all lanes on one line.
 template <int G, bool ZERO>
 __device__ __forceinline__ void load_tile(Tile<G, ZERO>& t, const Matrix& m, int tile, int kb,
                                           bool live) {
-  const int lane = live ? threadIdx.x & 63 : 0;
+  const uint32_t lane = (threadIdx.x & 63) & (live ? 63u : 0u);
   const int64_t at = (int64_t)tile * m.nkb + kb;
-  t.codes = ldg16(m.codes + (at * 64 + lane) * 16);
-  const int64_t gi = at * (128 / G) * 16 + (lane & 15);
+  const uint8_t* codes = m.codes + at * 1024;
+  t.codes = ldg16(codes + lane * 16);
+  const uint8_t* scales = m.scales + at * (128 / G) * 32;
+  const uint8_t* zeros = m.zeros + at * (128 / G) * 16;
 #pragma unroll
   for (int g = 0; g < 128 / G; ++g) {
-    t.scale[g] = *reinterpret_cast<const uint16_t*>(m.scales + (gi + 16 * g) * 2);
-    if (ZERO) t.zero[g] = m.zeros[gi + 16 * g];
+    t.scale[g] = *reinterpret_cast<const uint16_t*>(scales + 32 * g + (lane & 15) * 2);
+    if (ZERO) t.zero[g] = zeros[16 * g + (lane & 15)];
+  }
+}
+
+// 128 columns of the operand rows: `base` (scalar) is column 0 of the block,
+// `row` the lane's byte offset, `left` the columns from there on (a multiple of
+// 32).  Lanes with no row keep what they have: a result row depends on its own
+// operand row alone.  Columns past the end are zero.
+__device__ __forceinline__ void load_rows(bf16x8 (&x)[4], const uint8_t* base, uint32_t row,
+                                          bool has_row, int left) {
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    if (32 * s < left) {
+      if (has_row) x[s] = frag(*reinterpret_cast<const u32x4*>(base + 64 * s + row));
+    } else {
+      x[s] = frag(u32x4{0, 0, 0, 0});
+    }
   }
 }
 

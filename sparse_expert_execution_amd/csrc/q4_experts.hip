@@ -16,14 +16,15 @@ namespace {
 using namespace q4;
 
 // ---- units ------------------------------------------------------------------
-// One workgroup.  Pair i (thread i) is an expert's first if no earlier pair
-// names it; units are numbered by first appearance, their entries (pair
-// numbers, ascending) stored one after another.  Experts without a slot and
-// ids outside [0, E) give no unit.
-constexpr int kUnitThreads = kQ4MaxPairs;
+// One workgroup, thread i is pair i.  An expert's pairs are set in a bit mask
+// of its own in LDS, from which each of them reads the expert's first pair, its
+// own place and their number.  Units are numbered by first appearance, their
+// entries (pair numbers, ascending) stored one after another.  Experts without
+// a slot and ids outside [0, E) give no unit.
+constexpr int kUnitThreads = kQ4MaxPairs, kMaskWords = kQ4MaxPairs / 32;
 
 __global__ __launch_bounds__(kUnitThreads) void q4_units_kernel(Q4Experts a) {
-  __shared__ int16_t s_id[kQ4MaxPairs];
+  extern __shared__ uint32_t mask[];                  // [E][kMaskWords]
   __shared__ int s_sum[kUnitThreads / 64];
   __shared__ int16_t s_base[kQ4MaxPairs];
   const int i = threadIdx.x, lane = i & 63, wave = i >> 6;
@@ -33,16 +34,21 @@ __global__ __launch_bounds__(kUnitThreads) void q4_units_kernel(Q4Experts a) {
     if (id >= 0 && id < a.E) slot = a.slot_of ? a.slot_of[id] : id;
     if (slot < 0) id = -1;
   }
-  s_id[i] = (int16_t)id;
+  if (id >= 0)
+    for (int w = 0; w < kMaskWords; ++w) mask[id * kMaskWords + w] = 0;
+  __syncthreads();
+  if (id >= 0) atomicOr(&mask[id * kMaskWords + i / 32], 1u << (i % 32));
   __syncthreads();
   int first = -1, rank = 0, count = 0;
-  if (id >= 0)
-    for (int j = 0; j < a.P; ++j)
-      if (s_id[j] == id) {
-        if (first < 0) first = j;
-        if (j < i) ++rank;
-        ++count;
-      }
+  if (id >= 0) {
+#pragma unroll
+    for (int w = kMaskWords - 1; w >= 0; --w) {
+      const uint32_t v = mask[id * kMaskWords + w];
+      if (v) first = 32 * w + __builtin_ctz(v);
+      count += __popc(v);
+      rank += w < i / 32 ? __popc(v) : w == i / 32 ? __popc(v & ((1u << (i % 32)) - 1)) : 0;
+    }
+  }
   const bool lead = id >= 0 && first == i;
   const int packed = lead ? 1 << 16 | count : 0;
   const int inc = wave_scan_dpp(packed);
@@ -117,7 +123,8 @@ __device__ __forceinline__ void gate_up_columns(const Q4Experts& a, const uint8_
                                                 const int16_t* entries, int n_cols,
                                                 float (&red)[2][4][kGuWaves][64]) {
   constexpr int D = 2;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 4;
+  const int lane = threadIdx.x & 63, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int nkb = (a.H + 127) / 128;
   const Matrix mg{block + a.off[0], block + a.off[1], nullptr, nkb};
   const Matrix mu{block + a.off[2], block + a.off[3], nullptr, nkb};
@@ -128,7 +135,7 @@ __device__ __forceinline__ void gate_up_columns(const Q4Experts& a, const uint8_
     const int e = entries[c];
     token = e < a.P ? e / a.k : e - a.P;
   }
-  const uint16_t* xrow = a.x + (int64_t)token * a.H + 8 * q;
+  const uint32_t xrow = ((uint32_t)token * a.H + 8 * q) * 2;
   struct Block {
     Tile<G, false> t[2];
     bf16x8 x[1][4];
@@ -139,19 +146,18 @@ __device__ __forceinline__ void gate_up_columns(const Q4Experts& a, const uint8_
     const int kb = wave + (in ? it : 0) * kGuWaves;
     load_tile<G, false>(b.t[0], mg, tile, kb, in);
     load_tile<G, false>(b.t[1], mu, tile, kb, in);
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      u32x4 v = u32x4{0, 0, 0, 0};
-      if (in && live && 128 * kb + 32 * s + 8 * q < a.H)
-        v = *reinterpret_cast<const u32x4*>(xrow + 128 * kb + 32 * s);
-      b.x[0][s] = frag(v);
-    }
+    load_rows(b.x[0], reinterpret_cast<const uint8_t*>(a.x + 128 * kb), xrow, in && live,
+              a.H - 128 * kb);
   };
   float acc[2][1][TI];
 #pragma unroll
   for (int i = 0; i < TI; ++i) acc[0][0][i] = acc[1][0][i] = 0.f;
   if (n_it > 0) {
     Block b[D];
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+#pragma unroll
+      for (int s = 0; s < 4; ++s) b[d].x[0][s] = frag(u32x4{0, 0, 0, 0});
 #pragma unroll
     for (int d = 0; d < D - 1; ++d) load(b[d], d);
     for (int i0 = 0; i0 < n_it; i0 += D) {
@@ -196,9 +202,15 @@ __device__ __forceinline__ void gate_up_columns(const Q4Experts& a, const uint8_
 }
 
 template <int G, bool SMALL>
-__global__ __launch_bounds__(kGuWaves * 64, 4) void q4_gate_up_kernel(Q4Experts a) {
+__global__ __launch_bounds__(kGuWaves * 64, 4) void q4_gate_up_kernel(Q4Experts a, bool clear_y) {
   __shared__ float red[2][4][kGuWaves][64];
   __shared__ UnitList list;
+  if (clear_y) {
+    const int64_t all = (int64_t)gridDim.x * gridDim.y * kGuWaves * 64;
+    for (int64_t i = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kGuWaves * 64 + threadIdx.x;
+         i < (int64_t)a.T * a.H; i += all)
+      a.y[i] = 0.f;
+  }
   int4 u;
   const int16_t* entries;
   if (SMALL) {
@@ -225,10 +237,11 @@ __global__ __launch_bounds__(kGuWaves * 64, 4) void q4_gate_up_kernel(Q4Experts 
 
 // ---- down + combine -----------------------------------------------------------
 // One workgroup per 16 rows of y, for all tokens and experts, so the combine
-// needs neither atomics on memory nor another pass: the units' tiles are cut
-// into jobs (a unit, a slice of I) that go round the 16 waves; a wave adds a
-// job's gate-weighted result into a y tile of its own in LDS, and the 16
-// tiles are summed in wave order.
+// needs no other pass: the units' tiles are cut into jobs (a unit, a slice of I)
+// that go round the 16 waves; a wave adds a job's gate-weighted result into a y
+// tile of its own in LDS, and the 16 tiles are summed in wave order.  Where that
+// gives workgroups for half the compute units at most, two share the jobs of a
+// tile and add into a cleared y: 0 + a + b has one value whichever comes first.
 //
 // The three parts of h take three of the four quarters of the instruction's
 // rows (slot 4 part + entry), so four entries cost one instruction per 32
@@ -273,19 +286,19 @@ __global__ __launch_bounds__(kDnWaves * 64, 4) void q4_down_kernel(Q4Experts a, 
   const int nkb = (a.I + 127) / 128, tile = blockIdx.x;
   const int per = (nkb + cut - 1) / cut;              // column blocks of a job
   const int slices = (nkb + per - 1) / per, jobs = n_units * slices;
-  const int64_t plane = (int64_t)(a.P + a.T) * a.I;
+  const uint32_t plane = (uint32_t)(a.P + a.T) * a.I;
   float* mine = yl + (int64_t)wave * a.T * 16;
   const int part = n >> 2, e4 = n & 3;                // as an operand row
 
   // where the loads are: a job, four of its entries, a column block
-  int job = __builtin_amdgcn_readfirstlane(wave), c0 = 0, kb = 0, kend = 0, first = 0, count = 0;
+  const int stride = kDnWaves * gridDim.y;
+  int job = __builtin_amdgcn_readfirstlane(wave * gridDim.y + blockIdx.y), c0 = 0, kb = 0, kend = 0, first = 0, count = 0;
   Matrix m{nullptr, nullptr, nullptr, nkb};
-  const uint16_t* hrow = nullptr;
+  uint32_t hrow = 0;                                  // bytes
   bool live = false;
   auto chunk = [&]() {
     live = part < 3 && c0 + e4 < count;
-    hrow = a.h + 8 * q;
-    if (live) hrow += part * plane + (int64_t)entries[first + c0 + e4] * a.I;
+    if (live) hrow = (part * plane + (uint32_t)entries[first + c0 + e4] * a.I + 8 * q) * 2;
   };
   int k0 = 0;
   auto start = [&]() {
@@ -314,13 +327,8 @@ __global__ __launch_bounds__(kDnWaves * 64, 4) void q4_down_kernel(Q4Experts a, 
     const bool in = job < jobs;
     b.valid = in;
     load_tile<G, false>(b.t[0], m, tile, kb, in);
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      u32x4 v = u32x4{0, 0, 0, 0};
-      if (in && live && 128 * kb + 32 * s + 8 * q < a.I)
-        v = *reinterpret_cast<const u32x4*>(hrow + 128 * kb + 32 * s);
-      b.x[0][s] = frag(v);
-    }
+    load_rows(b.x[0], reinterpret_cast<const uint8_t*>(a.h + 128 * kb), hrow, in && live,
+              a.I - 128 * kb);
     b.flush = 0;
     b.at = first + c0;
     if (!in) return;
@@ -331,7 +339,7 @@ __global__ __launch_bounds__(kDnWaves * 64, 4) void q4_down_kernel(Q4Experts a, 
       if (c0 < count) {
         chunk();                                      // the tile again, from cache
       } else {
-        job += kDnWaves;
+        job += stride;
         if (job < jobs) start();
       }
     }
@@ -339,6 +347,10 @@ __global__ __launch_bounds__(kDnWaves * 64, 4) void q4_down_kernel(Q4Experts a, 
   if (job < jobs) {
     start();
     Block b[D];
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+#pragma unroll
+      for (int s = 0; s < 4; ++s) b[d].x[0][s] = frag(u32x4{0, 0, 0, 0});
 #pragma unroll
     for (int d = 0; d < D - 1; ++d) load(b[d]);
     float acc[1][1][4] = {};
@@ -372,22 +384,28 @@ __global__ __launch_bounds__(kDnWaves * 64, 4) void q4_down_kernel(Q4Experts a, 
     float v = 0.f;
 #pragma unroll
     for (int s = 0; s < kDnWaves; ++s) v += yl[(int64_t)s * a.T * 16 + j];
-    a.y[(int64_t)(j >> 4) * a.H + 16 * tile + (j & 15)] = v;
+    float* y = a.y + (int64_t)(j >> 4) * a.H + 16 * tile + (j & 15);
+    if (gridDim.y == 1) *y = v;
+    else __hip_atomic_fetch_add(y, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
 }
+
+// workgroups that share a tile of y (two: y is cleared by the gate / up launch)
+int down_split(const Q4Experts& a) { return a.H / 16 <= 128 ? 2 : 1; }
 
 template <int G, bool SMALL>
 hipError_t run_products(const Q4Experts& a, hipStream_t st) {
   const int most = (a.P < a.E ? a.P : a.E) + (a.shared ? 1 : 0);   // units at most
   hipLaunchKernelGGL((q4_gate_up_kernel<G, SMALL>), dim3(a.I / 16, most), dim3(kGuWaves * 64), 0,
-                     st, a);
+                     st, a, down_split(a) > 1);
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   // enough jobs for four rounds of the waves: an uneven last one costs little
-  int cut = (4 * kDnWaves + most - 1) / most;
+  const int split = down_split(a);
+  int cut = (4 * kDnWaves * split + most - 1) / most;
   const int nkb = (a.I + 127) / 128;
   cut = cut < 1 ? 1 : cut > nkb ? nkb : cut;
-  hipLaunchKernelGGL((q4_down_kernel<G, SMALL>), dim3(a.H / 16), dim3(kDnWaves * 64),
+  hipLaunchKernelGGL((q4_down_kernel<G, SMALL>), dim3(a.H / 16, split), dim3(kDnWaves * 64),
                      (size_t)kDnWaves * a.T * 16 * sizeof(float), st, a, cut);
   return hipGetLastError();
 }
@@ -395,7 +413,8 @@ hipError_t run_products(const Q4Experts& a, hipStream_t st) {
 template <int G>
 hipError_t run(const Q4Experts& a, hipStream_t st) {
   if (a.P <= kWavePairs) return run_products<G, true>(a, st);
-  hipLaunchKernelGGL(q4_units_kernel, dim3(1), dim3(kUnitThreads), 0, st, a);
+  hipLaunchKernelGGL(q4_units_kernel, dim3(1), dim3(kUnitThreads),
+                     (size_t)a.E * kMaskWords * 4, st, a);
   const hipError_t err = hipGetLastError();
   return err != hipSuccess ? err : run_products<G, false>(a, st);
 }
