@@ -431,8 +431,7 @@ int moe_q4_pack(const moe_q4_desc* desc, const uint8_t* codes, const void* scale
 /* moe_q4_linear: y[t][n] = sum over k of x[t][k] W[n][k], x BF16 as given,
  * fp32 accumulation in a fixed order.  Made for the few tokens of a decode
  * step; beyond 64 tokens the matrix is read again for every 64.
- *   x     device BF16 [T][cols], rows x_ld elements apart (fastest with cols
- *         and x_ld multiples of 8 and x 16-byte aligned)
+ *   x     device BF16 [T][cols], rows x_ld elements apart, any alignment
  *   block device, moe_q4_layout's
  *   y     device out [T][rows], rows y_ld elements apart, y_type
  *         MOE_WTYPE_F32 or MOE_WTYPE_BF16 (rounded once); must not overlap x

@@ -14,14 +14,14 @@ constexpr int kWaves = 8;
 // flight, and the KS partial sums of a tile meet in LDS, added in slice order.
 // x goes straight into the matrix operand's registers: lane (r, q) reads 16
 // bytes of the token in slot r, empty slots read nothing (one token costs
-// four lanes' loads, not 64).
-template <int NT, int TI, int RT, int G, bool ZERO, bool VEC>
+// four lanes' loads, not 64; what their registers hold reaches no other row).
+template <int NT, int TI, int RT, int G, bool ZERO>
 __global__ __launch_bounds__(kWaves * 64, NT == 4 ? 2 : NT == 2 ? 3 : 4) void
 q4_linear_kernel(Q4Linear a) {
   constexpr int D = NT == 1 && RT == 1 ? 3 : NT == 4 && G == 32 ? 1 : 2;
   extern __shared__ float red[];                      // [wave][RT * NT][TI][64]
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int q = lane >> 4;
+  const int lane = threadIdx.x & 63, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int KS = 1 << a.log_ks, slice = wave & (KS - 1), set = wave >> a.log_ks;
   const int rt0 = (blockIdx.x * (kWaves >> a.log_ks) + set) * RT;
   const int t0 = blockIdx.y * 16 * NT;
@@ -39,6 +39,10 @@ q4_linear_kernel(Q4Linear a) {
 #pragma unroll
   for (int r = 0; r < RT; ++r) tile[r] = rt0 + r < a.tiles ? rt0 + r : a.tiles - 1;
 
+  const uint16_t* row[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+    row[j] = a.x + (int64_t)(t0 + 16 * j + slot_token(lane & 15)) * a.x_ld + 8 * q;
   struct Block {
     Tile<G, ZERO> t[RT];
     bf16x8 x[NT][4];
@@ -49,27 +53,39 @@ q4_linear_kernel(Q4Linear a) {
     const int kb = slice + ((live ? it : 0) << a.log_ks);
 #pragma unroll
     for (int r = 0; r < RT; ++r) load_tile<G, ZERO>(b.t[r], m, tile[r], kb, live);
+    if (!live) return;
+    const int left = a.K - 128 * kb;
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      const int t = t0 + 16 * j + slot_token(lane & 15);
-      const uint16_t* row = a.x + (int64_t)t * a.x_ld;
+      if (t0 + 16 * j + slot_token(lane & 15) >= a.T) continue;   // an empty slot's row is not read
+      const uint16_t* src = row[j] + 128 * kb;
+      if (left >= 128) {
+        // a row may start at any element: 16-byte loads of any alignment
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const int k = 128 * kb + 32 * s + 8 * q;
-        u32x4 v = u32x4{0, 0, 0, 0};
-        if (VEC) {
-          if (live && t < a.T && k < a.K) v = *reinterpret_cast<const u32x4*>(row + k);
-        } else if (live && t < a.T) {
+        for (int s = 0; s < 4; ++s) __builtin_memcpy(&b.x[j][s], src + 32 * s, 16);
+      } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (k + i < a.K) v[i / 2] |= (uint32_t)row[k + i] << (16 * (i % 2));
+        for (int s = 0; s < 4; ++s) {
+          u32x4 v = u32x4{0, 0, 0, 0};
+          const int here = left - 32 * s - 8 * q;     // columns from this lane's first on
+          if (here >= 8) __builtin_memcpy(&v, src + 32 * s, 16);
+          else
+#pragma unroll
+            for (int i = 0; i < 7; ++i)
+              if (i < here) v[i / 2] |= (uint32_t)src[32 * s + i] << (16 * (i % 2));
+          b.x[j][s] = frag(v);
         }
-        b.x[j][s] = frag(v);
       }
     }
   };
 
   Block b[D];
+#pragma unroll
+  for (int d = 0; d < D; ++d)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int s = 0; s < 4; ++s) b[d].x[j][s] = frag(u32x4{0, 0, 0, 0});
 #pragma unroll
   for (int d = 0; d < D - 1; ++d) load(b[d], d);
   for (int i0 = 0; i0 < n_it; i0 += D) {
@@ -199,36 +215,31 @@ __global__ __launch_bounds__(256) void q4_pack_scales_kernel(const uint16_t* s, 
 }
 
 template <int NT, int TI, int RT, int G, bool ZERO>
-hipError_t run_linear(const Q4Linear& a, dim3 grid, bool vec, hipStream_t st) {
+hipError_t run_linear(const Q4Linear& a, dim3 grid, hipStream_t st) {
   const size_t lds = (size_t)kWaves * RT * NT * TI * 64 * sizeof(float);
-  if (vec)
-    hipLaunchKernelGGL((q4_linear_kernel<NT, TI, RT, G, ZERO, true>), grid, dim3(kWaves * 64),
-                       lds, st, a);
-  else
-    hipLaunchKernelGGL((q4_linear_kernel<NT, TI, RT, G, ZERO, false>), grid, dim3(kWaves * 64),
-                       lds, st, a);
+  hipLaunchKernelGGL((q4_linear_kernel<NT, TI, RT, G, ZERO>), grid, dim3(kWaves * 64), lds, st, a);
   return hipGetLastError();
 }
 
 template <int NT, int TI, int RT>
-hipError_t pick_group(const Q4Linear& a, int G, dim3 grid, bool vec, hipStream_t st) {
+hipError_t pick_group(const Q4Linear& a, int G, dim3 grid, hipStream_t st) {
   if (a.zeros) {
-    if (G == 32) return run_linear<NT, TI, RT, 32, true>(a, grid, vec, st);
-    if (G == 64) return run_linear<NT, TI, RT, 64, true>(a, grid, vec, st);
-    return run_linear<NT, TI, RT, 128, true>(a, grid, vec, st);
+    if (G == 32) return run_linear<NT, TI, RT, 32, true>(a, grid, st);
+    if (G == 64) return run_linear<NT, TI, RT, 64, true>(a, grid, st);
+    return run_linear<NT, TI, RT, 128, true>(a, grid, st);
   }
-  if (G == 32) return run_linear<NT, TI, RT, 32, false>(a, grid, vec, st);
-  if (G == 64) return run_linear<NT, TI, RT, 64, false>(a, grid, vec, st);
-  return run_linear<NT, TI, RT, 128, false>(a, grid, vec, st);
+  if (G == 32) return run_linear<NT, TI, RT, 32, false>(a, grid, st);
+  if (G == 64) return run_linear<NT, TI, RT, 64, false>(a, grid, st);
+  return run_linear<NT, TI, RT, 128, false>(a, grid, st);
 }
 
 template <int RT>
-hipError_t pick_tokens(const Q4Linear& a, int G, dim3 grid, bool vec, hipStream_t st) {
-  if (a.T <= 4) return pick_group<1, 1, RT>(a, G, grid, vec, st);
-  if (a.T <= 8) return pick_group<1, 2, RT>(a, G, grid, vec, st);
-  if (a.T <= 16) return pick_group<1, 4, RT>(a, G, grid, vec, st);
-  if (a.T <= 32) return pick_group<2, 4, 1>(a, G, grid, vec, st);
-  return pick_group<4, 4, 1>(a, G, grid, vec, st);
+hipError_t pick_tokens(const Q4Linear& a, int G, dim3 grid, hipStream_t st) {
+  if (a.T <= 4) return pick_group<1, 1, RT>(a, G, grid, st);
+  if (a.T <= 8) return pick_group<1, 2, RT>(a, G, grid, st);
+  if (a.T <= 16) return pick_group<1, 4, RT>(a, G, grid, st);
+  if (a.T <= 32) return pick_group<2, 4, 1>(a, G, grid, st);
+  return pick_group<4, 4, 1>(a, G, grid, st);
 }
 
 }  // namespace
@@ -237,13 +248,12 @@ hipError_t launch_q4_linear(Q4Linear a, int group, hipStream_t st) {
   a.tiles = (a.N + 15) / 16;
   a.nkb = (a.K + 127) / 128;
   a.log_ks = a.nkb >= 8 ? 3 : a.nkb >= 4 ? 2 : a.nkb >= 2 ? 1 : 0;
-  const bool vec = a.K % 8 == 0 && a.x_ld % 8 == 0 && (reinterpret_cast<uintptr_t>(a.x) & 15) == 0;
   const int sets = kWaves >> a.log_ks;
   const int nt = a.T <= 16 ? 1 : a.T <= 32 ? 2 : 4;
   const int rt = a.tiles >= 2048 && nt == 1 ? 2 : 1;
   const dim3 grid((a.tiles + sets * rt - 1) / (sets * rt), (a.T + 16 * nt - 1) / (16 * nt));
-  return rt == 2 ? pick_tokens<2>(a, group, grid, vec, st)
-                 : pick_tokens<1>(a, group, grid, vec, st);
+  return rt == 2 ? pick_tokens<2>(a, group, grid, st)
+                 : pick_tokens<1>(a, group, grid, st);
 }
 
 hipError_t launch_q4_quantize(const void* src, int bf16, int N, int K, int64_t ld, int group,

@@ -41,7 +41,10 @@ __device__ __forceinline__ v4f mfma(bf16x8 a, bf16x8 b, v4f c) {
 
 // a dword of eight codes -> eight BF16 values 16 + q
 __device__ __forceinline__ bf16x8 codes_plus16(uint32_t w) {
-  constexpr uint32_t m = 0x00780078u, one = 0x41804180u;
+  constexpr uint32_t m = 0x00780078u;
+  // in a vector register: an and-or takes one scalar constant, not two
+  uint32_t one;
+  asm("" : "=v"(one) : "0"(0x41804180u));
   return frag(u32x4{((w << 3) & m) | one, ((w >> 1) & m) | one, ((w >> 5) & m) | one,
                     ((w >> 9) & m) | one});
 }
