@@ -15,11 +15,17 @@ constexpr int kWaves = 8;
 // x goes straight into the matrix operand's registers: lane (r, q) reads 16
 // bytes of the token in slot r, empty slots read nothing (one token costs
 // four lanes' loads, not 64; what their registers hold reaches no other row).
-template <int NT, int TI, int RT, int G, bool ZERO>
+// More than four tokens (STAGE): neighbouring lanes of an operand are different
+// tokens, and a load of it costs a cache lookup per lane, so x goes through LDS,
+// 128 columns at a time and each wave for itself: loads run along the rows (16
+// lanes x 16 bytes), piece p of row i is kept at slot p ^ i % 16, from where the
+// operand is read without bank conflicts.
+template <int NT, int TI, int RT, int G, bool ZERO, bool STAGE>
 __global__ __launch_bounds__(kWaves * 64, NT == 4 ? 2 : NT == 2 ? 3 : 4) void
 q4_linear_kernel(Q4Linear a) {
   constexpr int D = NT == 1 && RT == 1 ? 3 : NT == 4 && G == 32 ? 1 : 2;
   extern __shared__ float red[];                      // [wave][RT * NT][TI][64]
+                                                      // STAGE, before: [wave][16 NT][16] pieces
   const int lane = threadIdx.x & 63, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int KS = 1 << a.log_ks, slice = wave & (KS - 1), set = wave >> a.log_ks;
@@ -39,10 +45,13 @@ q4_linear_kernel(Q4Linear a) {
 #pragma unroll
   for (int r = 0; r < RT; ++r) tile[r] = rt0 + r < a.tiles ? rt0 + r : a.tiles - 1;
 
-  const uint16_t* row[NT];
+  // a load's row and first column (within 128): operand order, or along the rows
+  constexpr int L = STAGE ? 4 * NT : NT;              // rows of a lane
+  int64_t row[L];
+  const int col = 8 * (STAGE ? lane & 15 : q);
 #pragma unroll
-  for (int j = 0; j < NT; ++j)
-    row[j] = a.x + (int64_t)(t0 + 16 * j + slot_token(lane & 15)) * a.x_ld + 8 * q;
+  for (int j = 0; j < L; ++j)
+    row[j] = (int64_t)(STAGE ? t0 + 4 * j + q : t0 + 16 * j + slot_token(lane & 15)) * a.x_ld + col;
   struct Block {
     Tile<G, ZERO> t[RT];
     bf16x8 x[NT][4];
@@ -56,27 +65,52 @@ q4_linear_kernel(Q4Linear a) {
     if (!live) return;
     const int left = a.K - 128 * kb;
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      if (t0 + 16 * j + slot_token(lane & 15) >= a.T) continue;   // an empty slot's row is not read
-      const uint16_t* src = row[j] + 128 * kb;
-      if (left >= 128) {
-        // a row may start at any element: 16-byte loads of any alignment
+    for (int j = 0; j < L; ++j) {
+      // a row past the last token is not read
+      if ((STAGE ? t0 + 4 * j + q : t0 + 16 * j + slot_token(lane & 15)) >= a.T) continue;
+      const uint16_t* src = a.x + row[j] + 128 * kb;
+      // a row may start at any element: 16-byte loads of any alignment
 #pragma unroll
-        for (int s = 0; s < 4; ++s) __builtin_memcpy(&b.x[j][s], src + 32 * s, 16);
-      } else {
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
+      for (int s = 0; s < 4 * NT / L; ++s) {
+        bf16x8& to = STAGE ? b.x[j / 4][j % 4] : b.x[j % NT][s];
+        if (left >= 128) {
+          __builtin_memcpy(&to, src + 32 * s, 16);
+        } else {
           u32x4 v = u32x4{0, 0, 0, 0};
-          const int here = left - 32 * s - 8 * q;     // columns from this lane's first on
+          const int here = left - 32 * s - col;       // columns from this lane's first on
           if (here >= 8) __builtin_memcpy(&v, src + 32 * s, 16);
           else
 #pragma unroll
             for (int i = 0; i < 7; ++i)
               if (i < here) v[i / 2] |= (uint32_t)src[32 * s + i] << (16 * (i % 2));
-          b.x[j][s] = frag(v);
+          to = frag(v);
         }
       }
     }
+  };
+
+  // STAGE: what the rows' loads brought -> operand order
+  u32x4* stage = reinterpret_cast<u32x4*>(red) + wave * 16 * NT * 16;
+  auto turn = [&](bf16x8 (&x)[NT][4]) {
+    if (!STAGE) return;
+#pragma unroll
+    for (int j = 0; j < 4 * NT; ++j) {
+      const int r = 4 * j + q;
+      stage[r * 16 + ((lane & 15) ^ (r & 15))] = __builtin_bit_cast(u32x4, x[j / 4][j % 4]);
+    }
+    // one wave's LDS accesses are done in order; the compiler must keep them so
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int r = 16 * j + slot_token(lane & 15);
+#pragma unroll
+      for (int s = 0; s < 4; ++s) x[j][s] = frag(stage[r * 16 + ((4 * s + q) ^ (r & 15))]);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
   };
 
   Block b[D];
@@ -93,9 +127,11 @@ q4_linear_kernel(Q4Linear a) {
     for (int d = 0; d < D; ++d) {
       if (i0 + d >= n_it) break;
       load(b[(d + D - 1) % D], i0 + d + D - 1);
+      turn(b[d].x);
       mul_tiles<RT, NT, TI, G, ZERO>(acc, b[d].t, b[d].x);
     }
   }
+  if (STAGE) __syncthreads();                         // the stages become the sums' buffer
 
 #pragma unroll
   for (int r = 0; r < RT; ++r)
@@ -216,8 +252,11 @@ __global__ __launch_bounds__(256) void q4_pack_scales_kernel(const uint16_t* s, 
 
 template <int NT, int TI, int RT, int G, bool ZERO>
 hipError_t run_linear(const Q4Linear& a, dim3 grid, hipStream_t st) {
-  const size_t lds = (size_t)kWaves * RT * NT * TI * 64 * sizeof(float);
-  hipLaunchKernelGGL((q4_linear_kernel<NT, TI, RT, G, ZERO>), grid, dim3(kWaves * 64), lds, st, a);
+  constexpr bool kStage = TI > 1;
+  constexpr size_t sums = (size_t)kWaves * RT * NT * TI * 64 * sizeof(float);
+  constexpr size_t stages = kStage ? (size_t)kWaves * NT * 4096 : 0;
+  hipLaunchKernelGGL((q4_linear_kernel<NT, TI, RT, G, ZERO, kStage>), grid, dim3(kWaves * 64),
+                     sums > stages ? sums : stages, st, a);
   return hipGetLastError();
 }
 
@@ -250,7 +289,7 @@ hipError_t launch_q4_linear(Q4Linear a, int group, hipStream_t st) {
   a.log_ks = a.nkb >= 8 ? 3 : a.nkb >= 4 ? 2 : a.nkb >= 2 ? 1 : 0;
   const int sets = kWaves >> a.log_ks;
   const int nt = a.T <= 16 ? 1 : a.T <= 32 ? 2 : 4;
-  const int rt = a.tiles >= 2048 && nt == 1 ? 2 : 1;
+  const int rt = a.tiles >= (a.T > 4 ? 512 : 2048) && nt == 1 ? 2 : 1;
   const dim3 grid((a.tiles + sets * rt - 1) / (sets * rt), (a.T + 16 * nt - 1) / (16 * nt));
   return rt == 2 ? pick_tokens<2>(a, group, grid, st)
                  : pick_tokens<1>(a, group, grid, st);

@@ -70,12 +70,15 @@ def _take(name, t, dtype, shape, device=None, rows=False):
     elif not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     index = t.get_device()
-    if device is None:
-        if index < 0 or index != torch.cuda.current_device():
-            raise ValueError(f"{name} is on {t.device}, which is not the current device")
-    elif index != device:
-        raise ValueError(f"{name} is on {t.device}, not on cuda:{device}")
+    if index != (device if device is not None else _current_device(index)):
+        where = "the current device" if device is None else f"cuda:{device}"
+        raise ValueError(f"{name} is on {t.device}, not on {where}")
     return index
+
+
+def _current_device(index):
+    """The current device's index; -2 for a host tensor's (-1), which no device has."""
+    return torch._C._cuda_getDevice() if index >= 0 else -2
 
 
 def _take_ws(ws, device):

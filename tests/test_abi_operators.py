@@ -158,7 +158,7 @@ def test_python_checks_name_the_argument():
     x = torch.zeros((3, 256), dtype=torch.bfloat16)
     wr = torch.zeros((8, 256), dtype=torch.bfloat16)
     z = torch.zeros((3, 8))
-    with pytest.raises(ValueError, match="x is on cpu"):
+    with pytest.raises(ValueError, match="x is on cpu, not on the current device"):
         ops.router_logits(d, x, wr, z)
     with pytest.raises(TypeError, match="x must be"):
         ops.router_logits(d, x.float(), wr, z)
