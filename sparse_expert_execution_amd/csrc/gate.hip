@@ -254,75 +254,119 @@ __global__ __launch_bounds__(kReduceWaves * 64) void gate_reduce_kernel(GateArgs
   }
 }
 
-// One wave per token.
-template <int M>
+// Four tokens per wave, as in gate_kernel; lane j of a row holds the token's
+// choices j, j + 16, ..  Their terms meet the others in LDS: a comparison of each
+// of a lane's experts with each choice cost more than the rest together.
+template <int C, int KB>
 __global__ __launch_bounds__(kGateWaves * 64) void gate_backward_kernel(GateBackward a) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  float b[M];
-  {
-    float f = 0.f;
-    if (a.dloss) {
-      const float n = (float)a.counts[a.E];
-      f = n > 0.f ? *a.dloss * (float)a.E / ((float)a.k * n * n) : 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < M; ++i) {
-      const int e = lane + 64 * i;
-      b[i] = a.dloss && e < a.E ? f * (float)a.counts[e] : 0.f;
-    }
+  constexpr int V = 4 * C;
+  __shared__ v4f s_dz[kGateWaves][4][C * 16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane & 15, row = lane >> 4;
+  const bool vec = a.E % 4 == 0;
+  float f = 0.f;
+  if (a.dloss) {
+    const float n = (float)a.counts[a.E];
+    f = n > 0.f ? *a.dloss * (float)a.E / ((float)a.k * n * n) : 0.f;
   }
-  for (int64_t t = (int64_t)blockIdx.x * kGateWaves + wave; t < a.T;
-       t += (int64_t)gridDim.x * kGateWaves) {
-    int id = -1;
-    float w = 0.f, dw = 0.f;
-    if (lane < a.k) {
-      id = a.ids[t * a.k + lane];
-      if (a.dw && id >= 0) { w = a.w[t * a.k + lane]; dw = a.dw[t * a.k + lane]; }
-    }
-    float* dz = a.dz + t * a.E;
-    if (__builtin_amdgcn_readfirstlane(id) < 0) {      // not routed
+  float b[V];
 #pragma unroll
-      for (int i = 0; i < M; ++i)
-        if (lane + 64 * i < a.E) dz[lane + 64 * i] = 0.f;
-      continue;
-    }
-    float p[M], m = -INFINITY, ps = 0.f;
+  for (int i = 0; i < V; ++i) {
+    const int e = 64 * (i / 4) + 4 * l + i % 4;
+    b[i] = a.dloss && e < a.E ? f * (float)a.counts[e] : 0.f;
+  }
+  for (int64_t t0 = ((int64_t)blockIdx.x * kGateWaves + wave) * 4; t0 < a.T;
+       t0 += (int64_t)gridDim.x * kGateWaves * 4) {
+    const int64_t t = t0 + row;
+    const bool in = t < a.T;
+    float p[V];
 #pragma unroll
-    for (int i = 0; i < M; ++i) {
-      const int e = lane + 64 * i;
-      p[i] = e < a.E ? a.z[t * a.E + e] : -INFINITY;
-      m = fmaxf(m, p[i]);
-    }
-    m = wave_max_dpp(m);
+    for (int c = 0; c < C; ++c) {
+      const int e = 64 * c + 4 * l;
+      const float* src = a.z + t * a.E + e;
 #pragma unroll
-    for (int i = 0; i < M; ++i) {
-      p[i] = lane + 64 * i < a.E ? expf(p[i] - m) : 0.f;
+      for (int i = 0; i < 4; ++i) p[4 * c + i] = -INFINITY;
+      if (vec) {
+        if (in && e < a.E) {
+          const float4 v = *reinterpret_cast<const float4*>(src);
+          p[4 * c] = v.x; p[4 * c + 1] = v.y; p[4 * c + 2] = v.z; p[4 * c + 3] = v.w;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (in && e + i < a.E) p[4 * c + i] = src[i];
+      }
+    }
+    int id[KB];
+    float w[KB], dw[KB], D = 0.f;
+#pragma unroll
+    for (int k = 0; k < KB; ++k) {
+      const int64_t at = t * a.k + 16 * k + l;
+      const bool has = in && 16 * k + l < a.k;
+      id[k] = has ? a.ids[at] : -1;
+      w[k] = dw[k] = 0.f;
+      if (a.dw && id[k] >= 0 && id[k] < a.E) {
+        w[k] = a.w[at];
+        dw[k] = a.dw[at];
+      }
+      D += w[k] * dw[k];
+    }
+    D = row_sum(D);
+    // not routed: the first choice is negative (lane 0 of the row has it)
+    const bool routed = __shfl(id[0], lane & 48, kWave) >= 0;
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < V; ++i) m = fmaxf(m, p[i]);
+    m = row_max(m);
+    const float top = routed ? m : 0.f;
+    float ps = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      p[i] = exp_neg(p[i] - top);
       ps += p[i];
     }
-    const float inv = 1.0f / wave_sum_dpp(ps);
+    const float inv = 1.0f / row_sum(ps);
     float pb = 0.f;
 #pragma unroll
-    for (int i = 0; i < M; ++i) {
+    for (int i = 0; i < V; ++i) {
       p[i] *= inv;
       pb += p[i] * b[i];
     }
-    const float B = wave_sum_dpp(pb), D = wave_sum_dpp(w * dw);
-    const float sub = a.renorm ? B : B + D;
-    const float add = a.renorm ? w * (dw - D) : w * dw;
-    float r[M];
+    const float B = row_sum(pb), sub = a.renorm ? B : B + D;
+    v4f r[C];
 #pragma unroll
-    for (int i = 0; i < M; ++i) r[i] = p[i] * (b[i] - sub);
-    if (a.dw)
-      for (int j = 0; j < a.k; ++j) {
-        const int e = __builtin_amdgcn_readlane(id, j);
-        const float v = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(add), j));
+    for (int i = 0; i < V; ++i) r[i / 4][i % 4] = routed ? p[i] * (b[i] - sub) : 0.f;
+    if (a.dw) {
+      // one wave's LDS accesses are done in order; the compiler must keep them so
 #pragma unroll
-        for (int i = 0; i < M; ++i)
-          if (lane + 64 * i == e) r[i] += v;
+      for (int c = 0; c < C; ++c) s_dz[wave][row][16 * c + l] = r[c];
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      float* mine = reinterpret_cast<float*>(s_dz[wave][row]);
+#pragma unroll
+      for (int k = 0; k < KB; ++k)
+        if (routed && id[k] >= 0 && id[k] < a.E)
+          __hip_atomic_fetch_add(mine + id[k], w[k] * (a.renorm ? dw[k] - D : dw[k]),
+                                 __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll
+      for (int c = 0; c < C; ++c) r[c] = s_dz[wave][row][16 * c + l];
+    }
+    if (!in) continue;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int e = 64 * c + 4 * l;
+      float* dst = a.dz + t * a.E + e;
+      if (vec) {
+        if (e < a.E) *reinterpret_cast<v4f*>(dst) = r[c];
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (e + i < a.E) dst[i] = r[c][i];
       }
-#pragma unroll
-    for (int i = 0; i < M; ++i)
-      if (lane + 64 * i < a.E) dz[lane + 64 * i] = r[i];
+    }
   }
 }
 
@@ -356,15 +400,22 @@ hipError_t launch_gate(const GateArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-hipError_t launch_gate_backward(const GateBackward& a, hipStream_t st) {
-  const int waves = a.T < 8192 ? a.T : 8192;
-  const dim3 g((waves + kGateWaves - 1) / kGateWaves), b(kGateWaves * 64);
-  if (a.E <= 64) hipLaunchKernelGGL(gate_backward_kernel<1>, g, b, 0, st, a);
-  else if (a.E <= 128) hipLaunchKernelGGL(gate_backward_kernel<2>, g, b, 0, st, a);
-  else if (a.E <= 256) hipLaunchKernelGGL(gate_backward_kernel<4>, g, b, 0, st, a);
-  else if (a.E <= 512) hipLaunchKernelGGL(gate_backward_kernel<8>, g, b, 0, st, a);
-  else hipLaunchKernelGGL(gate_backward_kernel<16>, g, b, 0, st, a);
+template <int C>
+hipError_t run_backward(const GateBackward& a, hipStream_t st) {
+  // four tokens a wave, up to eight waves a SIMD
+  const int quads = (a.T + 3) / 4, most = 8192;
+  const dim3 g(((quads < most ? quads : most) + kGateWaves - 1) / kGateWaves), b(kGateWaves * 64);
+  if (a.k <= 16) hipLaunchKernelGGL((gate_backward_kernel<C, 1>), g, b, 0, st, a);
+  else hipLaunchKernelGGL((gate_backward_kernel<C, 4>), g, b, 0, st, a);
   return hipGetLastError();
+}
+
+hipError_t launch_gate_backward(const GateBackward& a, hipStream_t st) {
+  return a.E <= 64    ? run_backward<1>(a, st)
+         : a.E <= 128 ? run_backward<2>(a, st)
+         : a.E <= 256 ? run_backward<4>(a, st)
+         : a.E <= 512 ? run_backward<8>(a, st)
+                      : run_backward<16>(a, st);
 }
 
 }  // namespace moe

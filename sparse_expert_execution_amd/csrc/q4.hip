@@ -21,9 +21,9 @@ constexpr int kWaves = 8;
 // lanes x 16 bytes), piece p of row i is kept at slot p ^ i % 16, from where the
 // operand is read without bank conflicts.
 template <int NT, int TI, int RT, int G, bool ZERO, bool STAGE>
-__global__ __launch_bounds__(kWaves * 64, NT == 4 ? 2 : NT == 2 ? 3 : 4) void
+__global__ __launch_bounds__(kWaves * 64, NT > 1 ? 2 : 4) void
 q4_linear_kernel(Q4Linear a) {
-  constexpr int D = NT == 1 && RT == 1 ? 3 : NT == 4 && G == 32 ? 1 : 2;
+  constexpr int D = NT == 1 && RT == 1 ? 3 : NT == 4 ? 1 : 2;
   extern __shared__ float red[];                      // [wave][RT * NT][TI][64]
                                                       // STAGE, before: [wave][16 NT][16] pieces
   const int lane = threadIdx.x & 63, q = lane >> 4;
@@ -272,15 +272,6 @@ hipError_t pick_group(const Q4Linear& a, int G, dim3 grid, hipStream_t st) {
   return run_linear<NT, TI, RT, 128, false>(a, grid, st);
 }
 
-template <int RT>
-hipError_t pick_tokens(const Q4Linear& a, int G, dim3 grid, hipStream_t st) {
-  if (a.T <= 4) return pick_group<1, 1, RT>(a, G, grid, st);
-  if (a.T <= 8) return pick_group<1, 2, RT>(a, G, grid, st);
-  if (a.T <= 16) return pick_group<1, 4, RT>(a, G, grid, st);
-  if (a.T <= 32) return pick_group<2, 4, 1>(a, G, grid, st);
-  return pick_group<4, 4, 1>(a, G, grid, st);
-}
-
 }  // namespace
 
 hipError_t launch_q4_linear(Q4Linear a, int group, hipStream_t st) {
@@ -289,10 +280,22 @@ hipError_t launch_q4_linear(Q4Linear a, int group, hipStream_t st) {
   a.log_ks = a.nkb >= 8 ? 3 : a.nkb >= 4 ? 2 : a.nkb >= 2 ? 1 : 0;
   const int sets = kWaves >> a.log_ks;
   const int nt = a.T <= 16 ? 1 : a.T <= 32 ? 2 : 4;
-  const int rt = a.tiles >= (a.T > 4 ? 512 : 2048) && nt == 1 ? 2 : 1;
+  // Row tiles a wave: every workgroup reads all of x, so with more tokens more
+  // of them pay, as long as a workgroup per compute unit is left.
+  const int rt = a.T <= 4 ? (a.tiles >= 2048 ? 2 : 1)
+                          : (nt == 4 && a.tiles >= 2048 ? 4 : a.tiles >= 512 ? 2 : 1);
   const dim3 grid((a.tiles + sets * rt - 1) / (sets * rt), (a.T + 16 * nt - 1) / (16 * nt));
-  return rt == 2 ? pick_tokens<2>(a, group, grid, st)
-                 : pick_tokens<1>(a, group, grid, st);
+  if (a.T <= 4) return rt == 2 ? pick_group<1, 1, 2>(a, group, grid, st)
+                               : pick_group<1, 1, 1>(a, group, grid, st);
+  if (a.T <= 8) return rt == 2 ? pick_group<1, 2, 2>(a, group, grid, st)
+                               : pick_group<1, 2, 1>(a, group, grid, st);
+  if (nt == 1) return rt == 2 ? pick_group<1, 4, 2>(a, group, grid, st)
+                              : pick_group<1, 4, 1>(a, group, grid, st);
+  if (nt == 2) return rt == 2 ? pick_group<2, 4, 2>(a, group, grid, st)
+                              : pick_group<2, 4, 1>(a, group, grid, st);
+  if (rt == 4) return pick_group<4, 4, 4>(a, group, grid, st);
+  return rt == 2 ? pick_group<4, 4, 2>(a, group, grid, st)
+                 : pick_group<4, 4, 1>(a, group, grid, st);
 }
 
 hipError_t launch_q4_quantize(const void* src, int bf16, int N, int K, int64_t ld, int group,

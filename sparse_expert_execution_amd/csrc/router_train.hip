@@ -283,12 +283,18 @@ hipError_t run_logits(const void* x, const void* w, int T, int H, int E, float* 
   return hipGetLastError();
 }
 
-// ---- W in operand order: [chunk of 64 h][32 e][tile j][part][64 lanes] -------
+// ---- operand orders -------------------------------------------------------------
+// W for dx: [chunk of 64 h][32 e][tile j][part][64 lanes]; dz^T for dW:
+// [32 tokens][16 e][part][64 lanes], three parts of it (dW is fp32: with two its
+// error was 2.5e-6 of its norm where an fp32 product has 5e-7).  One launch for
+// both: workgroups 0 .. nw - 1 take W, the others dz.
+constexpr int kZp = 3;
+
 template <bool RF32>
-__global__ __launch_bounds__(256) void pack_router_kernel(const void* __restrict__ w, int H, int E,
-                                                          u32x4* __restrict__ out) {
+__device__ __forceinline__ void pack_router(const void* __restrict__ w, int H, int E, int c,
+                                            int ks, int nks, u32x4* __restrict__ out) {
   constexpr int PL = RF32 ? 2 : 1;
-  const int c = blockIdx.x, ks = blockIdx.y, kq = threadIdx.x >> 6, hh = threadIdx.x & 63;
+  const int kq = threadIdx.x >> 6, hh = threadIdx.x & 63;
   const int h = 64 * c + hh;
   float v[8];
 #pragma unroll
@@ -304,9 +310,39 @@ __global__ __launch_bounds__(256) void pack_router_kernel(const void* __restrict
   u32x4 hi, lo;
   split8(v, hi, lo);
   const int j = (hh & 15) >> 2, r = 4 * (hh >> 4) + (hh & 3);
-  u32x4* o = out + ((((int64_t)c * gridDim.y + ks) * 4 + j) * PL) * 64 + 16 * kq + r;
+  u32x4* o = out + ((((int64_t)c * nks + ks) * 4 + j) * PL) * 64 + 16 * kq + r;
   o[0] = hi;
   if (RF32) o[64] = lo;
+}
+
+__device__ __forceinline__ void pack_dz(const float* __restrict__ dz, int T, int E, int net,
+                                        int64_t kt, u32x4* __restrict__ out) {
+  const int Ep = net * 16;
+  for (int i = threadIdx.x; i < Ep * 4; i += 256) {
+    const int e = i % Ep, kq = i / Ep;
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int64_t t = 32 * kt + 8 * kq + j;
+      v[j] = t < T && e < E ? dz[t * E + e] : 0.f;
+    }
+    u32x4 hi, mid, lo;
+    split8x3(v, hi, mid, lo);
+    u32x4* o = out + ((kt * net + e / 16) * kZp) * 64 + 16 * kq + e % 16;
+    o[0] = hi;
+    o[64] = mid;
+    o[128] = lo;
+  }
+}
+
+template <bool RF32>
+__global__ __launch_bounds__(256) void pack_kernel(const void* __restrict__ w,
+                                                   const float* __restrict__ dz, int T, int H,
+                                                   int E, int nw, int net, u32x4* __restrict__ wf,
+                                                   u32x4* __restrict__ zf) {
+  const int b = blockIdx.x, nks = (E + 31) / 32;
+  if (b < nw) pack_router<RF32>(w, H, E, b / nks, b % nks, nks, wf);
+  else pack_dz(dz, T, E, net, b - nw, zf);
 }
 
 // ---- dx -----------------------------------------------------------------------
@@ -412,32 +448,6 @@ __global__ __launch_bounds__(kDxWaves * 64) void router_dx_kernel(const float* _
       d[0] = o[0];
       d[1] = o[1];
     }
-  }
-}
-
-// ---- dz^T in operand order: [32 tokens][16 e][part][64 lanes] -----------------
-// Three parts here: dW is fp32, and with two its error was 2.5e-6 of its norm
-// where an fp32 product has 5e-7.
-constexpr int kZp = 3;
-
-__global__ __launch_bounds__(256) void pack_dz_kernel(const float* __restrict__ dz, int T, int E,
-                                                      int net, u32x4* __restrict__ out) {
-  const int64_t kt = blockIdx.x;
-  const int Ep = net * 16;
-  for (int i = threadIdx.x; i < Ep * 4; i += 256) {
-    const int e = i % Ep, kq = i / Ep;
-    float v[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int64_t t = 32 * kt + 8 * kq + j;
-      v[j] = t < T && e < E ? dz[t * E + e] : 0.f;
-    }
-    u32x4 hi, mid, lo;
-    split8x3(v, hi, mid, lo);
-    u32x4* o = out + ((kt * net + e / 16) * kZp) * 64 + 16 * kq + e % 16;
-    o[0] = hi;
-    o[64] = mid;
-    o[128] = lo;
   }
 }
 
@@ -548,7 +558,7 @@ __global__ __launch_bounds__(256) void sum_slices_kernel(const v4f* __restrict__
 }
 
 // experts per dW workgroup in tiles of 16, the number of those tiles, and the
-// token slices: a workgroup per compute unit where a slice has at least 8
+// token slices: a workgroup per compute unit where a slice has at least 4
 // steps of 32 tokens; short batches take fewer experts a workgroup instead
 struct DwPlan {
   int et, net, slices, per_slice;
@@ -556,7 +566,7 @@ struct DwPlan {
 DwPlan dw_plan(int T, int H, int E) {
   DwPlan p;
   const int nkt = T > 0 ? (T + 31) / 32 : 1, hx = (H + kDwH - 1) / kDwH;
-  const int most = nkt / 8 > 1 ? nkt / 8 : 1;
+  const int most = nkt / 4 > 1 ? nkt / 4 : 1;
   p.et = E > 64 ? 8 : E > 32 ? 4 : E > 16 ? 2 : 1;
   while (p.et > 1 && hx * ((E + 16 * p.et - 1) / (16 * p.et)) * most < 192) p.et /= 2;
   const int ey = (E + 16 * p.et - 1) / (16 * p.et), tiles = ey * hx;
@@ -636,24 +646,21 @@ hipError_t launch_router_backward(const RouterBackward& a, hipStream_t st) {
   const Ws L = carve(a.T, a.H, a.E);
   u32x4* wf = reinterpret_cast<u32x4*>(a.ws + L.wf);
   u32x4* zf = reinterpret_cast<u32x4*>(a.ws + L.zf);
-  hipError_t err = hipSuccess;
+  const DwPlan p = dw_plan(a.T, a.H, a.E);
+  const int nw = a.dx ? ((a.H + 63) / 64) * ((a.E + 31) / 32) : 0, nz = a.dw ? (a.T + 31) / 32 : 0;
+  if (a.router_f32)
+    hipLaunchKernelGGL(pack_kernel<true>, dim3(nw + nz), dim3(256), 0, st, a.w, a.dz, a.T, a.H,
+                       a.E, nw, p.net, wf, zf);
+  else
+    hipLaunchKernelGGL(pack_kernel<false>, dim3(nw + nz), dim3(256), 0, st, a.w, a.dz, a.T, a.H,
+                       a.E, nw, p.net, wf, zf);
+  hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return err;
   if (a.dx) {
-    const dim3 g((a.H + 63) / 64, (a.E + 31) / 32);
-    if (a.router_f32)
-      hipLaunchKernelGGL(pack_router_kernel<true>, g, dim3(256), 0, st, a.w, a.H, a.E, wf);
-    else
-      hipLaunchKernelGGL(pack_router_kernel<false>, g, dim3(256), 0, st, a.w, a.H, a.E, wf);
-    err = hipGetLastError();
-    if (err != hipSuccess) return err;
     err = a.router_f32 ? run_dx<true>(a, wf, st) : run_dx<false>(a, wf, st);
     if (err != hipSuccess) return err;
   }
   if (!a.dw) return err;
-  const DwPlan p = dw_plan(a.T, a.H, a.E);
-  hipLaunchKernelGGL(pack_dz_kernel, dim3((a.T + 31) / 32), dim3(256), 0, st, a.dz, a.T, a.E,
-                     p.net, zf);
-  err = hipGetLastError();
-  if (err != hipSuccess) return err;
   float* out = p.slices > 1 ? reinterpret_cast<float*>(a.ws + L.part) : a.dw;
   const dim3 g((a.H + kDwH - 1) / kDwH, p.net / p.et, p.slices), b(kDwWaves * 64);
   const uint16_t* x = static_cast<const uint16_t*>(a.x);

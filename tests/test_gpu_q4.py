@@ -110,6 +110,7 @@ LINEAR = [
     (33, 250, 640, 32, False, True), (64, 96, 1536, 128, True, False),
     (65, 50, 264, 64, True, False), (200, 40, 384, 32, False, False),
     (1, 40000, 256, 128, False, False), (3, 33000, 200, 32, True, True),
+    (20, 8200, 136, 128, True, False), (50, 8193, 131, 64, False, True), (9, 8192, 72, 32, False, False),
     (40, 32784, 128, 64, False, False), (64, 32800, 300, 32, True, False),
 ]
 
