@@ -85,7 +85,7 @@ __global__ __launch_bounds__(WAVES * 64) void gate_kernel(GateArgs a) {
   for (int64_t t0 = ((int64_t)wave * gridDim.x + blockIdx.x) * 4; t0 < a.T;
        t0 += (int64_t)gridDim.x * WAVES * 4) {
     const int64_t t = t0 + (lane >> 4);
-    const bool in = t < a.T && (!a.mask || a.mask[t]);
+    bool in = t < a.T;
     float v[V];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -104,10 +104,12 @@ __global__ __launch_bounds__(WAVES * 64) void gate_kernel(GateArgs a) {
           if (in && e + i < a.E) v[4 * c + i] = src[i];
       }
     }
+    if (a.mask) in = in && a.mask[in ? t : 0];        // padding: as a row of -inf
     float m = -INFINITY;
     uint32_t nan = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
+      v[i] = in ? v[i] : -INFINITY;
       v[i] += 0.f;                                    // a logit of -0 ranks with +0
       nan |= v[i] != v[i];
       m = fmaxf(m, v[i]);
@@ -263,22 +265,10 @@ __global__ __launch_bounds__(kGateWaves * 64) void gate_backward_kernel(GateBack
   __shared__ v4f s_dz[kGateWaves][4][C * 16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane & 15, row = lane >> 4;
   const bool vec = a.E % 4 == 0;
-  float f = 0.f;
-  if (a.dloss) {
-    const float n = (float)a.counts[a.E];
-    f = n > 0.f ? *a.dloss * (float)a.E / ((float)a.k * n * n) : 0.f;
-  }
-  float b[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = 64 * (i / 4) + 4 * l + i % 4;
-    b[i] = a.dloss && e < a.E ? f * (float)a.counts[e] : 0.f;
-  }
-  for (int64_t t0 = ((int64_t)blockIdx.x * kGateWaves + wave) * 4; t0 < a.T;
-       t0 += (int64_t)gridDim.x * kGateWaves * 4) {
-    const int64_t t = t0 + row;
+  float p[V], w[KB], dw[KB], b[V];
+  int id[KB];
+  auto load = [&](int64_t t) {
     const bool in = t < a.T;
-    float p[V];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int e = 64 * c + 4 * l;
@@ -296,18 +286,33 @@ __global__ __launch_bounds__(kGateWaves * 64) void gate_backward_kernel(GateBack
           if (in && e + i < a.E) p[4 * c + i] = src[i];
       }
     }
-    int id[KB];
-    float w[KB], dw[KB], D = 0.f;
 #pragma unroll
     for (int k = 0; k < KB; ++k) {
       const int64_t at = t * a.k + 16 * k + l;
       const bool has = in && 16 * k + l < a.k;
       id[k] = has ? a.ids[at] : -1;
-      w[k] = dw[k] = 0.f;
-      if (a.dw && id[k] >= 0 && id[k] < a.E) {
-        w[k] = a.w[at];
-        dw[k] = a.dw[at];
-      }
+      w[k] = has && a.dw ? a.w[at] : 0.f;
+      dw[k] = has && a.dw ? a.dw[at] : 0.f;
+    }
+  };
+  int64_t t0 = ((int64_t)blockIdx.x * kGateWaves + wave) * 4;
+  load(t0 + row);                                     // before the wait for the counts
+  {
+    const float n = a.dloss ? (float)a.counts[a.E] : 0.f;
+    const float f = n > 0.f ? *a.dloss * (float)a.E / ((float)a.k * n * n) : 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = 64 * (i / 4) + 4 * l + i % 4;
+      b[i] = a.dloss && e < a.E ? f * (float)a.counts[e] : 0.f;
+    }
+  }
+  for (;;) {
+    const int64_t t = t0 + row;
+    const bool in = t < a.T;
+    float D = 0.f;
+#pragma unroll
+    for (int k = 0; k < KB; ++k) {
+      if (id[k] < 0 || id[k] >= a.E) w[k] = dw[k] = 0.f;
       D += w[k] * dw[k];
     }
     D = row_sum(D);
@@ -354,19 +359,23 @@ __global__ __launch_bounds__(kGateWaves * 64) void gate_backward_kernel(GateBack
 #pragma unroll
       for (int c = 0; c < C; ++c) r[c] = s_dz[wave][row][16 * c + l];
     }
-    if (!in) continue;
+    if (in) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int e = 64 * c + 4 * l;
-      float* dst = a.dz + t * a.E + e;
-      if (vec) {
-        if (e < a.E) *reinterpret_cast<v4f*>(dst) = r[c];
-      } else {
+      for (int c = 0; c < C; ++c) {
+        const int e = 64 * c + 4 * l;
+        float* dst = a.dz + t * a.E + e;
+        if (vec) {
+          if (e < a.E) *reinterpret_cast<v4f*>(dst) = r[c];
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (e + i < a.E) dst[i] = r[c][i];
+          for (int i = 0; i < 4; ++i)
+            if (e + i < a.E) dst[i] = r[c][i];
+        }
       }
     }
+    t0 += (int64_t)gridDim.x * kGateWaves * 4;
+    if (t0 >= a.T) return;
+    load(t0 + row);
   }
 }
 
