@@ -13,8 +13,7 @@ constexpr int kWaves = 8;
 // columns; a wave walks its slice's column blocks with D - 1 blocks' loads in
 // flight, and the KS partial sums of a tile meet in LDS, added in slice order.
 // x goes straight into the matrix operand's registers: lane (r, q) reads 16
-// bytes of the token in slot r, empty slots read nothing (one token costs
-// four lanes' loads, not 64; what their registers hold reaches no other row).
+// bytes of the token in slot r.
 // More than four tokens (STAGE): neighbouring lanes of an operand are different
 // tokens, and a load of it costs a cache lookup per lane, so x goes through LDS,
 // 128 columns at a time and each wave for itself: loads run along the rows (16
@@ -45,48 +44,57 @@ q4_linear_kernel(Q4Linear a) {
 #pragma unroll
   for (int r = 0; r < RT; ++r) tile[r] = rt0 + r < a.tiles ? rt0 + r : a.tiles - 1;
 
-  // a load's row and first column (within 128): operand order, or along the rows
+  // a load's row and first column (within 128): operand order, or along the rows.
+  // Rows past the last token read the last one: what they give reaches no result
+  // of another row.
   constexpr int L = STAGE ? 4 * NT : NT;              // rows of a lane
   int64_t row[L];
   const int col = 8 * (STAGE ? lane & 15 : q);
 #pragma unroll
-  for (int j = 0; j < L; ++j)
-    row[j] = (int64_t)(STAGE ? t0 + 4 * j + q : t0 + 16 * j + slot_token(lane & 15)) * a.x_ld + col;
+  for (int j = 0; j < L; ++j) {
+    const int t = STAGE ? t0 + 4 * j + q : t0 + 16 * j + slot_token(lane & 15);
+    row[j] = (int64_t)(t < a.T ? t : a.T - 1) * a.x_ld + col;
+  }
   struct Block {
     Tile<G, ZERO> t[RT];
     bf16x8 x[NT][4];
   };
-  const int n_it = (a.nkb - slice + KS - 1) >> a.log_ks;
+  // whole column blocks, in a pipeline without a branch around any load (the
+  // waits count the loads issued after); a last partial one follows
+  const int full = a.K / 128;
+  const int n_it = slice < full ? (full - slice + KS - 1) >> a.log_ks : 0;
   auto load = [&](Block& b, int it) {
-    const bool live = it < n_it;                      // n_it >= 1: KS <= nkb
+    const bool live = it < n_it;
     const int kb = slice + ((live ? it : 0) << a.log_ks);
 #pragma unroll
     for (int r = 0; r < RT; ++r) load_tile<G, ZERO>(b.t[r], m, tile[r], kb, live);
-    if (!live) return;
-    const int left = a.K - 128 * kb;
 #pragma unroll
     for (int j = 0; j < L; ++j) {
-      // a row past the last token is not read
-      if ((STAGE ? t0 + 4 * j + q : t0 + 16 * j + slot_token(lane & 15)) >= a.T) continue;
-      const uint16_t* src = a.x + row[j] + 128 * kb;
       // a row may start at any element: 16-byte loads of any alignment
+      const uint16_t* src = a.x + 128 * kb + (STAGE || live ? row[j] : 0);
+#pragma unroll
+      for (int s = 0; s < 4 * NT / L; ++s)
+        __builtin_memcpy(STAGE ? &b.x[j / 4][j % 4] : &b.x[j % NT][s], src + 32 * s, 16);
+    }
+  };
+  auto load_last = [&](Block& b) {
+    const int left = a.K - 128 * full;
+#pragma unroll
+    for (int r = 0; r < RT; ++r) load_tile<G, ZERO>(b.t[r], m, tile[r], full, true);
+#pragma unroll
+    for (int j = 0; j < L; ++j)
 #pragma unroll
       for (int s = 0; s < 4 * NT / L; ++s) {
-        bf16x8& to = STAGE ? b.x[j / 4][j % 4] : b.x[j % NT][s];
-        if (left >= 128) {
-          __builtin_memcpy(&to, src + 32 * s, 16);
-        } else {
-          u32x4 v = u32x4{0, 0, 0, 0};
-          const int here = left - 32 * s - col;       // columns from this lane's first on
-          if (here >= 8) __builtin_memcpy(&v, src + 32 * s, 16);
-          else
+        const uint16_t* src = a.x + 128 * full + row[j] + 32 * s;
+        const int here = left - 32 * s - col;         // columns from this lane's first on
+        u32x4 v = u32x4{0, 0, 0, 0};
+        if (here >= 8) __builtin_memcpy(&v, src, 16);
+        else
 #pragma unroll
-            for (int i = 0; i < 7; ++i)
-              if (i < here) v[i / 2] |= (uint32_t)src[32 * s + i] << (16 * (i % 2));
-          to = frag(v);
-        }
+          for (int i = 0; i < 7; ++i)
+            if (i < here) v[i / 2] |= (uint32_t)src[i] << (16 * (i % 2));
+        (STAGE ? b.x[j / 4][j % 4] : b.x[j % NT][s]) = frag(v);
       }
-    }
   };
 
   // STAGE: what the rows' loads brought -> operand order
@@ -113,23 +121,25 @@ q4_linear_kernel(Q4Linear a) {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
   };
 
-  Block b[D];
+  if (n_it > 0) {
+    Block b[D];
 #pragma unroll
-  for (int d = 0; d < D; ++d)
+    for (int d = 0; d < D - 1; ++d) load(b[d], d);
+    for (int i0 = 0; i0 < n_it; i0 += D) {
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int s = 0; s < 4; ++s) b[d].x[j][s] = frag(u32x4{0, 0, 0, 0});
-#pragma unroll
-  for (int d = 0; d < D - 1; ++d) load(b[d], d);
-  for (int i0 = 0; i0 < n_it; i0 += D) {
-#pragma unroll
-    for (int d = 0; d < D; ++d) {
-      if (i0 + d >= n_it) break;
-      load(b[(d + D - 1) % D], i0 + d + D - 1);
-      turn(b[d].x);
-      mul_tiles<RT, NT, TI, G, ZERO>(acc, b[d].t, b[d].x);
+      for (int d = 0; d < D; ++d) {
+        if (i0 + d >= n_it) break;
+        load(b[(d + D - 1) % D], i0 + d + D - 1);
+        turn(b[d].x);
+        mul_tiles<RT, NT, TI, G, ZERO>(acc, b[d].t, b[d].x);
+      }
     }
+  }
+  if (full < a.nkb && slice == (full & (KS - 1))) {
+    Block b;
+    load_last(b);
+    turn(b.x);
+    mul_tiles<RT, NT, TI, G, ZERO>(acc, b.t, b.x);
   }
   if (STAGE) __syncthreads();                         // the stages become the sums' buffer
 

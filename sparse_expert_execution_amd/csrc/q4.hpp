@@ -95,20 +95,26 @@ __device__ __forceinline__ void load_tile(Tile<G, ZERO>& t, const Matrix& m, int
   }
 }
 
-// 128 columns of the operand rows: `base` (scalar) is column 0 of the block,
-// `row` the lane's byte offset, `left` the columns from there on (a multiple of
-// 32).  Lanes with no row keep what they have: a result row depends on its own
-// operand row alone.  Columns past the end are zero.
-__device__ __forceinline__ void load_rows(bf16x8 (&x)[4], const uint8_t* base, uint32_t row,
-                                          bool has_row, int left) {
+// A buffer of `bytes` bytes for loads whose lanes with nothing to read take an
+// offset past its end: they read zeros, without a branch.  A branch around a load
+// would make every later wait count without it, i.e. wait for loads meant to stay
+// in flight (the down product took 60 us with branches where it takes 45).
+typedef __amdgpu_buffer_rsrc_t Buffer;
+constexpr uint32_t kNowhere = 0x80000000u;            // bytes < 2^31
+__device__ __forceinline__ Buffer buffer_of(const void* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00027000);
+}
+
+// 128 columns of the operand rows: `row` is the lane's byte offset (or kNowhere),
+// `base` (scalar) that of the block's first column, `left` the columns from there
+// on (a multiple of 32; zeros past them).
+__device__ __forceinline__ void load_rows(bf16x8 (&x)[4], Buffer b, uint32_t row, uint32_t base,
+                                          int left) {
 #pragma unroll
-  for (int s = 0; s < 4; ++s) {
-    if (32 * s < left) {
-      if (has_row) x[s] = frag(*reinterpret_cast<const u32x4*>(base + 64 * s + row));
-    } else {
-      x[s] = frag(u32x4{0, 0, 0, 0});
-    }
-  }
+  for (int s = 0; s < 4; ++s)
+    x[s] = __builtin_bit_cast(
+        bf16x8, __builtin_amdgcn_raw_buffer_load_b128(b, 32 * s < left ? row : kNowhere,
+                                                      base + 64 * s, 0));
 }
 
 __device__ __forceinline__ uint32_t dword(const uint4& v, int i) {

@@ -135,7 +135,8 @@ __device__ __forceinline__ void gate_up_columns(const Q4Experts& a, const uint8_
     const int e = entries[c];
     token = e < a.P ? e / a.k : e - a.P;
   }
-  const uint32_t xrow = ((uint32_t)token * a.H + 8 * q) * 2;
+  const uint32_t xrow = live ? ((uint32_t)token * a.H + 8 * q) * 2 : kNowhere;
+  const Buffer xb = buffer_of(a.x, (uint32_t)a.T * a.H * 2);
   struct Block {
     Tile<G, false> t[2];
     bf16x8 x[1][4];
@@ -146,18 +147,13 @@ __device__ __forceinline__ void gate_up_columns(const Q4Experts& a, const uint8_
     const int kb = wave + (in ? it : 0) * kGuWaves;
     load_tile<G, false>(b.t[0], mg, tile, kb, in);
     load_tile<G, false>(b.t[1], mu, tile, kb, in);
-    load_rows(b.x[0], reinterpret_cast<const uint8_t*>(a.x + 128 * kb), xrow, in && live,
-              a.H - 128 * kb);
+    load_rows(b.x[0], xb, xrow, 256 * kb, in ? a.H - 128 * kb : 0);
   };
   float acc[2][1][TI];
 #pragma unroll
   for (int i = 0; i < TI; ++i) acc[0][0][i] = acc[1][0][i] = 0.f;
   if (n_it > 0) {
     Block b[D];
-#pragma unroll
-    for (int d = 0; d < D; ++d)
-#pragma unroll
-      for (int s = 0; s < 4; ++s) b[d].x[0][s] = frag(u32x4{0, 0, 0, 0});
 #pragma unroll
     for (int d = 0; d < D - 1; ++d) load(b[d], d);
     for (int i0 = 0; i0 < n_it; i0 += D) {
@@ -237,8 +233,8 @@ __global__ __launch_bounds__(kGuWaves * 64, 4) void q4_gate_up_kernel(Q4Experts 
 
 // ---- down + combine -----------------------------------------------------------
 // One workgroup per 16 rows of y, for all tokens and experts, so the combine
-// needs no other pass: the units' tiles are cut into jobs (a unit, a slice of I)
-// that go round the 16 waves; a wave adds a job's gate-weighted result into a y
+// needs no other pass: the units' tiles are cut into jobs (an item, i.e. up to
+// four entries of a unit, and a slice of I) that go round the 16 waves; a wave adds a job's gate-weighted result into a y
 // tile of its own in LDS, and the 16 tiles are summed in wave order.  Where that
 // gives workgroups for half the compute units at most, two share the jobs of a
 // tile and add into a cleared y: 0 + a + b has one value whichever comes first.
@@ -257,6 +253,7 @@ __global__ __launch_bounds__(kDnWaves * 64, 4) void q4_down_kernel(Q4Experts a, 
   __shared__ int4 s_unit[SMALL ? 1 : kPairs + 1];
   __shared__ int16_t s_entry[SMALL ? 1 : kPairs + kQ4MaxTokens];
   __shared__ float s_w[kPairs + kQ4MaxTokens];
+  __shared__ int s_item[kPairs + kQ4MaxTokens / 4], s_items;   // q4_items at most
   __shared__ uint8_t s_token[kPairs + kQ4MaxTokens];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 4, n = lane & 15;
   // by pair: the token and the gate weight
@@ -283,87 +280,97 @@ __global__ __launch_bounds__(kDnWaves * 64, 4) void q4_down_kernel(Q4Experts a, 
     entries = s_entry;
   }
   n_units = __builtin_amdgcn_readfirstlane(n_units);
+  // items: unit << 10 | first of its entries' place in the unit.  Whole units as
+  // jobs left waves waiting for those that had the units of many entries.
+  if (wave == 0) {
+    int at = 0;
+    for (int i0 = 0; i0 < n_units; i0 += 64) {
+      const int i = i0 + lane;
+      const int chunks = i < n_units ? (units[i].z + 3) / 4 : 0;
+      const int inc = wave_scan_dpp(chunks);
+      for (int c = 0; c < chunks; ++c) s_item[at + inc - chunks + c] = i << 10 | 4 * c;
+      at += __builtin_amdgcn_readlane(inc, 63);
+    }
+    if (lane == 0) s_items = at;
+  }
+  __syncthreads();
+  const int n_items = __builtin_amdgcn_readfirstlane(s_items);
   const int nkb = (a.I + 127) / 128, tile = blockIdx.x;
   const int per = (nkb + cut - 1) / cut;              // column blocks of a job
-  const int slices = (nkb + per - 1) / per, jobs = n_units * slices;
+  const int slices = (nkb + per - 1) / per;
   const uint32_t plane = (uint32_t)(a.P + a.T) * a.I;
   float* mine = yl + (int64_t)wave * a.T * 16;
   const int part = n >> 2, e4 = n & 3;                // as an operand row
 
-  // where the loads are: a job, four of its entries, a column block
-  const int stride = kDnWaves * gridDim.y;
-  int job = __builtin_amdgcn_readfirstlane(wave * gridDim.y + blockIdx.y), c0 = 0, kb = 0, kend = 0, first = 0, count = 0;
-  Matrix m{nullptr, nullptr, nullptr, nkb};
-  uint32_t hrow = 0;                                  // bytes
-  bool live = false;
-  auto chunk = [&]() {
-    live = part < 3 && c0 + e4 < count;
-    if (live) hrow = (part * plane + (uint32_t)entries[first + c0 + e4] * a.I + 8 * q) * 2;
-  };
-  int k0 = 0;
+  // Where the loads are: item `ii`, slice `sl` of its columns, column block kb.
+  // All of it is the same for the whole wave, and said so to the compiler, which
+  // else keeps it in vector registers.
+  const auto uni = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+  const int stride = kDnWaves * gridDim.y, item_step = uni(stride / slices);
+  const int slice_step = uni(stride - item_step * slices);
+  const int job0 = uni(wave) * gridDim.y + blockIdx.y;
+  int ii = uni(job0 / slices), sl = uni(job0 - ii * slices);
+  int kb = 0, kend = 0, first = 0, count = 0, slot = 0;
+  const Buffer hb = buffer_of(a.h, plane * 6);
+  uint32_t hrow = kNowhere;                           // bytes
   auto start = [&]() {
-    const int ui = job / slices;
-    k0 = (job - ui * slices) * per;
-    kend = min(k0 + per, nkb);
-    kb = k0;
-    c0 = 0;
-    const int4 u = units[ui];
-    const int slot = __builtin_amdgcn_readfirstlane(u.x);
-    first = __builtin_amdgcn_readfirstlane(u.y);
-    count = __builtin_amdgcn_readfirstlane(u.z);
-    const uint8_t* block = slot < 0 ? a.shared : a.pool + (int64_t)slot * a.expert_bytes;
-    m.codes = block + a.off[4];
-    m.scales = block + a.off[5];
-    chunk();
+    const int item = uni(s_item[ii]), c0 = item & 1023;
+    const int4 u = units[item >> 10];
+    slot = uni(u.x);
+    first = uni(u.y) + c0;
+    count = min(4, uni(u.z) - c0);
+    kb = sl * per;
+    kend = min(kb + per, nkb);
+    hrow = part < 3 && e4 < count
+               ? (part * plane + (uint32_t)entries[first + e4] * a.I + 8 * q) * 2
+               : kNowhere;
   };
 
-  // a column block in flight; at the last one of a chunk: its entries' number
+  // a column block in flight; at the last one of a job: its entries and number
   struct Block {
     Tile<G, false> t[1];
     bf16x8 x[1][4];
     int valid, flush, at;
   };
   auto load = [&](Block& b) {
-    const bool in = job < jobs;
+    ii = uni(ii);
+    kb = uni(kb);
+    const bool in = ii < n_items;
     b.valid = in;
+    const uint8_t* block = slot < 0 ? a.shared : a.pool + (int64_t)uni(slot) * a.expert_bytes;
+    const Matrix m{block + a.off[4], block + a.off[5], nullptr, nkb};
     load_tile<G, false>(b.t[0], m, tile, kb, in);
-    load_rows(b.x[0], reinterpret_cast<const uint8_t*>(a.h + 128 * kb), hrow, in && live,
-              a.I - 128 * kb);
+    load_rows(b.x[0], hb, hrow, 256 * kb, in ? a.I - 128 * kb : 0);
     b.flush = 0;
-    b.at = first + c0;
+    b.at = first;
     if (!in) return;
     if (++kb == kend) {
-      b.flush = min(4, count - c0);
-      c0 += 4;
-      kb = k0;
-      if (c0 < count) {
-        chunk();                                      // the tile again, from cache
-      } else {
-        job += stride;
-        if (job < jobs) start();
+      b.flush = count;
+      ii += item_step;
+      sl += slice_step;
+      if (sl >= slices) {
+        sl -= slices;
+        ++ii;
       }
+      if (ii < n_items) start();
     }
   };
-  if (job < jobs) {
+  if (ii < n_items) {
     start();
     Block b[D];
-#pragma unroll
-    for (int d = 0; d < D; ++d)
-#pragma unroll
-      for (int s = 0; s < 4; ++s) b[d].x[0][s] = frag(u32x4{0, 0, 0, 0});
 #pragma unroll
     for (int d = 0; d < D - 1; ++d) load(b[d]);
     float acc[1][1][4] = {};
     for (bool more = true; more;) {
 #pragma unroll
       for (int d = 0; d < D; ++d) {
-        if (!b[d].valid) {
+        if (!uni(b[d].valid)) {
           more = false;
           break;
         }
         load(b[(d + D - 1) % D]);
         mul_tiles<1, 1, 4, G, false>(acc, b[d].t, b[d].x);
-        if (b[d].flush == 0) continue;
+        if (uni(b[d].flush) == 0) continue;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           // small parts first; lanes 0..15 hold the sum of the three
