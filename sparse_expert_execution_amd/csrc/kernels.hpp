@@ -165,7 +165,7 @@ struct Q4Experts {
   int32_t* n_units;
   int4* units;             // [P + 1] slot (-1: the shared expert), first entry, entries, 0
   int16_t* entries;        // [P + T] pair numbers, P + t for the shared expert
-  uint16_t* h;             // [3][P + T][I] h as three BF16 parts
+  uint16_t* h;             // [P + T][I / 8][4][8] h as three BF16 parts (the fourth unused)
   int P;                   // set by the launcher
 };
 hipError_t launch_q4_experts(Q4Experts a, int group, hipStream_t st);

@@ -106,15 +106,17 @@ __device__ __forceinline__ Buffer buffer_of(const void* p, uint32_t bytes) {
 }
 
 // 128 columns of the operand rows: `row` is the lane's byte offset (or kNowhere),
-// `base` (scalar) that of the block's first column, `left` the columns from there
-// on (a multiple of 32; zeros past them).
+// `base` (scalar) that of the block's first column, STEP the bytes from one 32
+// columns to the next, `left` the columns from there on (a multiple of 32; zeros
+// past them).
+template <int STEP>
 __device__ __forceinline__ void load_rows(bf16x8 (&x)[4], Buffer b, uint32_t row, uint32_t base,
                                           int left) {
 #pragma unroll
   for (int s = 0; s < 4; ++s)
     x[s] = __builtin_bit_cast(
         bf16x8, __builtin_amdgcn_raw_buffer_load_b128(b, 32 * s < left ? row : kNowhere,
-                                                      base + 64 * s, 0));
+                                                      base + STEP * s, 0));
 }
 
 __device__ __forceinline__ uint32_t dword(const uint4& v, int i) {

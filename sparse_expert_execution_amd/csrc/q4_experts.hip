@@ -147,7 +147,7 @@ __device__ __forceinline__ void gate_up_columns(const Q4Experts& a, const uint8_
     const int kb = wave + (in ? it : 0) * kGuWaves;
     load_tile<G, false>(b.t[0], mg, tile, kb, in);
     load_tile<G, false>(b.t[1], mu, tile, kb, in);
-    load_rows(b.x[0], xb, xrow, 256 * kb, in ? a.H - 128 * kb : 0);
+    load_rows<64>(b.x[0], xb, xrow, 256 * kb, in ? a.H - 128 * kb : 0);
   };
   float acc[2][1][TI];
 #pragma unroll
@@ -183,17 +183,18 @@ __device__ __forceinline__ void gate_up_columns(const Q4Experts& a, const uint8_
     const int col = result_token(l, i);
     if (col >= n_cols) continue;
     const float h = g / (1.f + expf(-g)) * u;
-    // h as three BF16 parts, all 24 bits of it: the down product takes them
-    // side by side, so y keeps fp32's accuracy rather than BF16's
-    const int64_t at = (int64_t)entries[col] * a.I + 16 * tile + (l & 15);
-    const int64_t plane = (int64_t)(a.P + a.T) * a.I;
+    // h as three BF16 parts, all 24 bits of it: y keeps fp32's accuracy rather
+    // than BF16's.  Laid out [entry][32 of I][8 of I][part, 4][8], as four
+    // neighbouring lanes of the down product read it.
+    const int row = 16 * tile + (l & 15);
+    const int64_t at = (int64_t)entries[col] * a.I * 4 + (row >> 3) * 32 + (row & 7);
     const __bf16 h0 = (__bf16)h;
     const float r1 = h - (float)h0;
     const __bf16 h1 = (__bf16)r1;
     const __bf16 h2 = (__bf16)(r1 - (float)h1);
     a.h[at] = __builtin_bit_cast(uint16_t, h0);
-    a.h[at + plane] = __builtin_bit_cast(uint16_t, h1);
-    a.h[at + 2 * plane] = __builtin_bit_cast(uint16_t, h2);
+    a.h[at + 8] = __builtin_bit_cast(uint16_t, h1);
+    a.h[at + 16] = __builtin_bit_cast(uint16_t, h2);
   }
 }
 
@@ -239,9 +240,11 @@ __global__ __launch_bounds__(kGuWaves * 64, 4) void q4_gate_up_kernel(Q4Experts 
 // gives workgroups for half the compute units at most, two share the jobs of a
 // tile and add into a cleared y: 0 + a + b has one value whichever comes first.
 //
-// The three parts of h take three of the four quarters of the instruction's
-// rows (slot 4 part + entry), so four entries cost one instruction per 32
-// columns, and a lane's result i is entry i of part l / 16.
+// Operand row 4 e + part is part `part` of h of the job's entry e (the fourth row
+// of an entry is empty), so one instruction takes four entries, four neighbouring
+// lanes of a load read 64 bytes of one entry (rows of h apart from each other were
+// a cache access per lane), and a lane's results 0, 1, 2 are the parts of entry
+// l / 16.
 constexpr int kDnWaves = 16;
 
 template <int G, bool SMALL>
@@ -298,9 +301,8 @@ __global__ __launch_bounds__(kDnWaves * 64, 4) void q4_down_kernel(Q4Experts a, 
   const int nkb = (a.I + 127) / 128, tile = blockIdx.x;
   const int per = (nkb + cut - 1) / cut;              // column blocks of a job
   const int slices = (nkb + per - 1) / per;
-  const uint32_t plane = (uint32_t)(a.P + a.T) * a.I;
   float* mine = yl + (int64_t)wave * a.T * 16;
-  const int part = n >> 2, e4 = n & 3;                // as an operand row
+  const int e4 = n >> 2, part = n & 3;                // as an operand row
 
   // Where the loads are: item `ii`, slice `sl` of its columns, column block kb.
   // All of it is the same for the whole wave, and said so to the compiler, which
@@ -311,7 +313,7 @@ __global__ __launch_bounds__(kDnWaves * 64, 4) void q4_down_kernel(Q4Experts a, 
   const int job0 = uni(wave) * gridDim.y + blockIdx.y;
   int ii = uni(job0 / slices), sl = uni(job0 - ii * slices);
   int kb = 0, kend = 0, first = 0, count = 0, slot = 0;
-  const Buffer hb = buffer_of(a.h, plane * 6);
+  const Buffer hb = buffer_of(a.h, (uint32_t)(a.P + a.T) * a.I * 8);
   uint32_t hrow = kNowhere;                           // bytes
   auto start = [&]() {
     const int item = uni(s_item[ii]), c0 = item & 1023;
@@ -322,7 +324,7 @@ __global__ __launch_bounds__(kDnWaves * 64, 4) void q4_down_kernel(Q4Experts a, 
     kb = sl * per;
     kend = min(kb + per, nkb);
     hrow = part < 3 && e4 < count
-               ? (part * plane + (uint32_t)entries[first + e4] * a.I + 8 * q) * 2
+               ? (uint32_t)entries[first + e4] * a.I * 8 + q * 64 + part * 16
                : kNowhere;
   };
 
@@ -340,7 +342,7 @@ __global__ __launch_bounds__(kDnWaves * 64, 4) void q4_down_kernel(Q4Experts a, 
     const uint8_t* block = slot < 0 ? a.shared : a.pool + (int64_t)uni(slot) * a.expert_bytes;
     const Matrix m{block + a.off[4], block + a.off[5], nullptr, nkb};
     load_tile<G, false>(b.t[0], m, tile, kb, in);
-    load_rows(b.x[0], hb, hrow, 256 * kb, in ? a.I - 128 * kb : 0);
+    load_rows<256>(b.x[0], hb, hrow, 1024 * kb, in ? a.I - 128 * kb : 0);
     b.flush = 0;
     b.at = first;
     if (!in) return;
@@ -353,6 +355,7 @@ __global__ __launch_bounds__(kDnWaves * 64, 4) void q4_down_kernel(Q4Experts a, 
         ++ii;
       }
       if (ii < n_items) start();
+      else kb = 0;        // loads past the last job: a block of this tile, not one past it
     }
   };
   if (ii < n_items) {
@@ -360,7 +363,7 @@ __global__ __launch_bounds__(kDnWaves * 64, 4) void q4_down_kernel(Q4Experts a, 
     Block b[D];
 #pragma unroll
     for (int d = 0; d < D - 1; ++d) load(b[d]);
-    float acc[1][1][4] = {};
+    float acc[1][1][3] = {};
     for (bool more = true; more;) {
 #pragma unroll
       for (int d = 0; d < D; ++d) {
@@ -369,20 +372,17 @@ __global__ __launch_bounds__(kDnWaves * 64, 4) void q4_down_kernel(Q4Experts a, 
           break;
         }
         load(b[(d + D - 1) % D]);
-        mul_tiles<1, 1, 4, G, false>(acc, b[d].t, b[d].x);
-        if (uni(b[d].flush) == 0) continue;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          // small parts first; lanes 0..15 hold the sum of the three
-          const float v =
-              acc[0][0][i] + (__shfl(acc[0][0][i], n + 16, kWave) +
-                              __shfl(acc[0][0][i], n + 32, kWave));
-          acc[0][0][i] = 0.f;
-          if (q == 0 && i < b[d].flush) {
-            const int e = entries[b[d].at + i];
-            mine[s_token[e] * 16 + n] += s_w[e] * v;
-          }
+        mul_tiles<1, 1, 3, G, false>(acc, b[d].t, b[d].x);
+        const int flush = uni(b[d].flush);
+        if (flush == 0) continue;
+        if (q < flush) {
+          const int e = entries[b[d].at + q];
+          // an LDS add: a token that names one expert twice is two entries here
+          __hip_atomic_fetch_add(&mine[s_token[e] * 16 + n],
+                                 s_w[e] * (acc[0][0][0] + (acc[0][0][1] + acc[0][0][2])),
+                                 __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
         }
+        acc[0][0][0] = acc[0][0][1] = acc[0][0][2] = 0.f;
       }
     }
   }

@@ -404,6 +404,34 @@ def test_experts_in_a_graph_beside_eager_calls(ops):
         assert np.array_equal(y.cpu().numpy(), eager)
 
 
+def test_experts_in_a_pool_that_fills_its_allocation(ops):
+    """The last expert's blocks end with the pool (153 pages of 2 MiB): the loads
+    that run ahead of the last job stay inside it.  Bytes are random codes under a
+    scale of 1 (BF16 0x3F80) by construction of the sections."""
+    H, I, E, k, T = 2048, 768, 128, 8, 64
+    desc = ops.make_desc(H, I, E, k, wtype="int4_g64")
+    off, n = ops.expert_layout(desc)
+    assert n * E == 153 << 21
+    pool = torch.randint(0, 256, (E, n), dtype=torch.uint8, device="cuda")
+    ends = list(off[2::2]) + [n]
+    for m in range(3):
+        part = pool[:, off[2 * m + 1]:ends[m]]
+        part.view(E, -1, 2)[..., 0] = 0x80
+        part.view(E, -1, 2)[..., 1] = 0x3A             # 2^-10
+    ids = torch.stack([torch.randperm(E, device="cuda")[:k] for _ in range(T)]).to(torch.int32)
+    ids[0] = torch.arange(E - k, E)
+    w = torch.rand((T, k), device="cuda")
+    x = torch.randn((T, H), device="cuda").to(torch.bfloat16)
+    ws = ops.workspace(desc, T, ops.MODE_DECODE)
+    ys = []
+    for _ in range(3):
+        y = torch.empty((T, H), device="cuda")
+        ops.decode(desc, x, ids, w, pool.view(-1), y, ws)
+        torch.cuda.synchronize()
+        ys.append(y)
+    assert torch.isfinite(ys[0]).all() and torch.equal(ys[0], ys[1]) and torch.equal(ys[0], ys[2])
+
+
 def test_experts_from_the_cache(ops):
     """INT4 experts through the expert cache: planned, filled, decoded."""
     H, I, E, k = 256, 96, 12, 3
