@@ -113,7 +113,7 @@ GateWs gate_ws(const moe_desc* d, int T) {
   const size_t parts = moe::gate_parts(T), row = parts * d->n_experts * 4;
   size_t o = 0;
   w.ticket = o; o = align_up(o + 4);
-  w.share = o; o = align_up(o + 16 * 4);
+  w.share = o; o = align_up(o + 64 * 4);
   w.n = o; o = align_up(o + parts * 4);
   w.s = o; o = align_up(o + row);
   w.c = o; o = align_up(o + row);

@@ -94,7 +94,7 @@ struct GateArgs {
   float* part_s;           // [gate_parts(T)][E]
   int32_t* part_c;         // [gate_parts(T)][E]
   int32_t* part_n;         // [gate_parts(T)]
-  float* share;            // [16]
+  float* share;            // [64]
   unsigned* ticket;
 };
 // workgroups (and rows of partial sums) of the gate: 16 tokens each until 256

@@ -24,7 +24,7 @@ using namespace q4;
 constexpr int kUnitThreads = kQ4MaxPairs, kMaskWords = kQ4MaxPairs / 32;
 
 __global__ __launch_bounds__(kUnitThreads) void q4_units_kernel(Q4Experts a) {
-  extern __shared__ uint32_t mask[];                  // [E][kMaskWords]
+  extern __shared__ uint32_t mask[];                  // [kMaskWords][E]: few bank conflicts
   __shared__ int s_sum[kUnitThreads / 64];
   __shared__ int16_t s_base[kQ4MaxPairs];
   const int i = threadIdx.x, lane = i & 63, wave = i >> 6;
@@ -34,16 +34,15 @@ __global__ __launch_bounds__(kUnitThreads) void q4_units_kernel(Q4Experts a) {
     if (id >= 0 && id < a.E) slot = a.slot_of ? a.slot_of[id] : id;
     if (slot < 0) id = -1;
   }
-  if (id >= 0)
-    for (int w = 0; w < kMaskWords; ++w) mask[id * kMaskWords + w] = 0;
+  for (int w = i; w < kMaskWords * a.E; w += kUnitThreads) mask[w] = 0;
   __syncthreads();
-  if (id >= 0) atomicOr(&mask[id * kMaskWords + i / 32], 1u << (i % 32));
+  if (id >= 0) atomicOr(&mask[i / 32 * a.E + id], 1u << (i % 32));
   __syncthreads();
   int first = -1, rank = 0, count = 0;
   if (id >= 0) {
 #pragma unroll
     for (int w = kMaskWords - 1; w >= 0; --w) {
-      const uint32_t v = mask[id * kMaskWords + w];
+      const uint32_t v = mask[w * a.E + id];
       if (v) first = 32 * w + __builtin_ctz(v);
       count += __popc(v);
       rank += w < i / 32 ? __popc(v) : w == i / 32 ? __popc(v & ((1u << (i % 32)) - 1)) : 0;

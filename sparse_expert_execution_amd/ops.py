@@ -297,16 +297,31 @@ def q4_pack(desc, codes, scales, block, zeros=None, stream=None):
 def q4_linear(desc, x, block, y, stream=None):
     """moe_q4_linear: y [T, rows] = x [T, cols] @ W.T; x bf16, y float32 or bf16,
     both with contiguous rows (any row stride)."""
+    rows, cols = desc.rows, desc.cols
     T = x.shape[0]
-    dev = _take("x", x, torch.bfloat16, (T, desc.cols), rows=True)
-    if y.dtype not in (torch.float32, torch.bfloat16):
+    dev, x_ld, y_ld = x.get_device(), cols, rows
+    # what a decode step passes, checked in few calls; anything else one by one,
+    # which names what is wrong or finds rows that are further apart
+    if dev < 0 or dev != torch._C._cuda_getDevice() or x.dtype is not torch.bfloat16 \
+            or x.shape != (T, cols) or not x.is_contiguous():
+        dev = _take("x", x, torch.bfloat16, (T, cols), rows=True)
+        x_ld = max(x.stride(0), cols)
+    y_type = _Y_TYPE.get(y.dtype)
+    if y_type is None:
         raise TypeError("y must be float32 or bfloat16")
-    _take("y", y, y.dtype, (T, desc.rows), dev, rows=True)
-    _take_block(desc, block, dev)
-    check(lib().moe_q4_linear(ctypes.byref(desc), _at(x), max(x.stride(0), desc.cols), T,
-                              _at(block), _at(y),
-                              _lib.WTYPE_F32 if y.dtype == torch.float32 else _lib.WTYPE_BF16,
-                              max(y.stride(0), desc.rows), _on(stream, dev)), "moe_q4_linear")
+    if y.get_device() != dev or y.shape != (T, rows) or not y.is_contiguous():
+        _take("y", y, y.dtype, (T, rows), dev, rows=True)
+        y_ld = max(y.stride(0), rows)
+    if block.get_device() != dev or block.dtype is not torch.uint8 or not block.is_contiguous() \
+            or block.numel() < _q4_bytes(rows, cols, desc.group, desc.has_zero):
+        _take_block(desc, block, dev)
+    st = lib().moe_q4_linear(ctypes.byref(desc), x.data_ptr(), x_ld, T, block.data_ptr(),
+                             y.data_ptr(), y_type, y_ld, _on(stream, dev))
+    if st:
+        check(st, "moe_q4_linear")
+
+
+_Y_TYPE = {torch.float32: _lib.WTYPE_F32, torch.bfloat16: _lib.WTYPE_BF16}
 
 
 def dequant_mxfp4(codes, scales, out, stream=None):
