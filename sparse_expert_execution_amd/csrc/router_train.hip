@@ -351,15 +351,14 @@ __global__ __launch_bounds__(256) void pack_kernel(const void* __restrict__ w,
 constexpr int kDxWaves = 8;
 
 template <int NTL, bool RF32>
-__global__ __launch_bounds__(kDxWaves * 64) void router_dx_kernel(const float* __restrict__ dz,
-                                                                  const u32x4* __restrict__ wf,
-                                                                  int T, int H, int E,
-                                                                  uint16_t* __restrict__ dx) {
+__device__ __forceinline__ void router_dx(const float* __restrict__ dz,
+                                          const u32x4* __restrict__ wf, int T, int H, int E,
+                                          uint16_t* __restrict__ dx, int bx, int by, int ny) {
   constexpr int PL = RF32 ? 2 : 1;
   extern __shared__ u32x4 sb[];                       // [e block][token tile][part][64]
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, q = lane >> 4;
   const int nks = (E + 31) / 32, nc = (H + 63) / 64;
-  const int64_t t0 = (int64_t)blockIdx.x * 16 * NTL;
+  const int64_t t0 = (int64_t)bx * 16 * NTL;
   const bool vec = E % 4 == 0;
   // four pieces' loads in flight before the first is used
   for (int i0 = wave; i0 < nks * NTL; i0 += 4 * kDxWaves) {
@@ -400,7 +399,7 @@ __global__ __launch_bounds__(kDxWaves * 64) void router_dx_kernel(const float* _
     }
   }
   __syncthreads();
-  for (int c = blockIdx.y * kDxWaves + wave; c < nc; c += gridDim.y * kDxWaves) {
+  for (int c = by * kDxWaves + wave; c < nc; c += ny * kDxWaves) {
     v4f acc[4][NTL];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -467,17 +466,18 @@ __device__ __forceinline__ uint32_t pack_hi(uint32_t a, uint32_t b) {
 }
 
 template <int ET>
-__global__ __launch_bounds__(kDwWaves * 64, 2) void router_dw_kernel(
-    const uint16_t* __restrict__ x, const u32x4* __restrict__ zf, int T, int H, int E, int net,
-    int per_slice, float* __restrict__ out) {
+__device__ __forceinline__ void router_dw(const uint16_t* __restrict__ x,
+                                          const u32x4* __restrict__ zf, int T, int H, int E,
+                                          int net, int per_slice, float* __restrict__ out, int bx,
+                                          int by, int bz) {
   constexpr int kStage = ET * kZp * 64, kCopies = (kStage + kDwWaves * 64 - 1) / (kDwWaves * 64);
   __shared__ u32x4 sa[2][kStage];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, q = lane >> 4;
   const int nkt = (T + 31) / 32;
-  const int k0 = blockIdx.z * per_slice, k1 = min(nkt, k0 + per_slice);
-  const int h = blockIdx.x * kDwH + wave * 64 + 4 * n;
+  const int k0 = bz * per_slice, k1 = min(nkt, k0 + per_slice);
+  const int h = bx * kDwH + wave * 64 + 4 * n;
   const bool hin = h < H;
-  const u32x4* zsrc = zf + (int64_t)blockIdx.y * ET * kZp * 64;
+  const u32x4* zsrc = zf + (int64_t)by * ET * kZp * 64;
 
   u32x4 za[kCopies];
   uint2 xr[8];
@@ -535,16 +535,47 @@ __global__ __launch_bounds__(kDwWaves * 64, 2) void router_dw_kernel(
     if (kt + 1 < k1) stage(buf ^ 1);
   }
   if (!hin) return;
-  float* o = out + (int64_t)blockIdx.z * E * H;
+  float* o = out + (int64_t)bz * E * H;
 #pragma unroll
   for (int e = 0; e < ET; ++e)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int row = (blockIdx.y * ET + e) * 16 + 4 * q + i;
+      const int row = (by * ET + e) * 16 + 4 * q + i;
       if (row < E)
         *reinterpret_cast<v4f*>(o + (int64_t)row * H + h) =
             v4f{acc[e][0][i], acc[e][1][i], acc[e][2][i], acc[e][3][i]};
     }
+}
+
+template <int NTL, bool RF32>
+__global__ __launch_bounds__(kDxWaves * 64) void router_dx_kernel(const float* dz, const u32x4* wf,
+                                                                  int T, int H, int E,
+                                                                  uint16_t* dx) {
+  router_dx<NTL, RF32>(dz, wf, T, H, E, dx, blockIdx.x, blockIdx.y, gridDim.y);
+}
+
+template <int ET>
+__global__ __launch_bounds__(kDwWaves * 64, 2) void router_dw_kernel(const uint16_t* x,
+                                                                     const u32x4* zf, int T,
+                                                                     int H, int E, int net,
+                                                                     int per_slice, float* out) {
+  router_dw<ET>(x, zf, T, H, E, net, per_slice, out, blockIdx.x, blockIdx.y, blockIdx.z);
+}
+
+// Both in one launch, where neither fills the chip: workgroups 0 .. ndx - 1 are
+// dx's (gx of them side by side), the others dW's.
+template <int ET, bool RF32>
+__global__ __launch_bounds__(kDxWaves * 64, 2) void router_both_kernel(
+    const uint16_t* x, const float* dz, const u32x4* wf, const u32x4* zf, int T, int H, int E,
+    int gx, int gy, int hx, int ey, int net, int per_slice, uint16_t* dx, float* out) {
+  static_assert(kDxWaves == kDwWaves, "one block size");
+  const int b = blockIdx.x, ndx = gx * gy;
+  if (b < ndx) {
+    router_dx<2, RF32>(dz, wf, T, H, E, dx, b % gx, b / gx, gy);
+  } else {
+    const int d = b - ndx;
+    router_dw<ET>(x, zf, T, H, E, net, per_slice, out, d % hx, d / hx % ey, d / (hx * ey));
+  }
 }
 
 // the token slices' partial sums, in slice order
@@ -594,25 +625,53 @@ Ws carve(int T, int H, int E) {
   return w;
 }
 
+// dx: tokens per workgroup in tiles of 16 (dz of all experts in 128 KB of LDS, and
+// few enough that short batches still spread over the compute units) and the
+// workgroups side by side over the chunks of 64 h
+struct DxPlan {
+  int ntl, gx, gy;
+  size_t lds;
+};
+DxPlan dx_plan(int T, int H, int E) {
+  DxPlan p;
+  const int nks = (E + 31) / 32, nc = (H + 63) / 64;
+  p.ntl = nks <= 8 ? 8 : nks <= 16 ? 4 : 2;
+  while (p.ntl > 2 && (T + 16 * p.ntl - 1) / (16 * p.ntl) < 64) p.ntl /= 2;
+  p.gx = (T + 16 * p.ntl - 1) / (16 * p.ntl);
+  const int most = (nc + kDxWaves - 1) / kDxWaves, gy = 256 / p.gx;
+  p.gy = gy < 1 ? 1 : gy > most ? most : gy;
+  p.lds = (size_t)nks * p.ntl * 2 * 1024;
+  return p;
+}
+
 template <bool RF32>
-hipError_t run_dx(const RouterBackward& a, const u32x4* wf, hipStream_t st) {
-  const int nks = (a.E + 31) / 32, nc = (a.H + 63) / 64;
-  // tokens per workgroup: dz of all experts in 128 KB of LDS, and few enough
-  // tokens that short batches still spread over the compute units
-  int ntl = nks <= 8 ? 8 : nks <= 16 ? 4 : 2;
-  while (ntl > 2 && (a.T + 16 * ntl - 1) / (16 * ntl) < 64) ntl /= 2;
-  const int gx = (a.T + 16 * ntl - 1) / (16 * ntl);
-  int gy = 256 / gx;
-  const int most = (nc + kDxWaves - 1) / kDxWaves;
-  gy = gy < 1 ? 1 : gy > most ? most : gy;
-  const size_t lds = (size_t)nks * ntl * 2 * 1024;
-  const dim3 g(gx, gy), b(kDxWaves * 64);
-  if (ntl == 8)
-    hipLaunchKernelGGL((router_dx_kernel<8, RF32>), g, b, lds, st, a.dz, wf, a.T, a.H, a.E, a.dx);
-  else if (ntl == 4)
-    hipLaunchKernelGGL((router_dx_kernel<4, RF32>), g, b, lds, st, a.dz, wf, a.T, a.H, a.E, a.dx);
+hipError_t run_dx(const RouterBackward& a, const DxPlan& p, const u32x4* wf, hipStream_t st) {
+  const dim3 g(p.gx, p.gy), b(kDxWaves * 64);
+  if (p.ntl == 8)
+    hipLaunchKernelGGL((router_dx_kernel<8, RF32>), g, b, p.lds, st, a.dz, wf, a.T, a.H, a.E, a.dx);
+  else if (p.ntl == 4)
+    hipLaunchKernelGGL((router_dx_kernel<4, RF32>), g, b, p.lds, st, a.dz, wf, a.T, a.H, a.E, a.dx);
   else
-    hipLaunchKernelGGL((router_dx_kernel<2, RF32>), g, b, lds, st, a.dz, wf, a.T, a.H, a.E, a.dx);
+    hipLaunchKernelGGL((router_dx_kernel<2, RF32>), g, b, p.lds, st, a.dz, wf, a.T, a.H, a.E, a.dx);
+  return hipGetLastError();
+}
+
+template <int ET>
+hipError_t run_dw(const RouterBackward& a, const DwPlan& p, const u32x4* zf, float* out,
+                  hipStream_t st) {
+  const dim3 g((a.H + kDwH - 1) / kDwH, p.net / p.et, p.slices);
+  hipLaunchKernelGGL(router_dw_kernel<ET>, g, dim3(kDwWaves * 64), 0, st,
+                     static_cast<const uint16_t*>(a.x), zf, a.T, a.H, a.E, p.net, p.per_slice, out);
+  return hipGetLastError();
+}
+
+template <int ET, bool RF32>
+hipError_t run_both(const RouterBackward& a, const DxPlan& d, const DwPlan& p, const u32x4* wf,
+                    const u32x4* zf, float* out, hipStream_t st) {
+  const int hx = (a.H + kDwH - 1) / kDwH, ey = p.net / p.et;
+  hipLaunchKernelGGL((router_both_kernel<ET, RF32>), dim3(d.gx * d.gy + hx * ey * p.slices),
+                     dim3(kDxWaves * 64), d.lds, st, static_cast<const uint16_t*>(a.x), a.dz, wf,
+                     zf, a.T, a.H, a.E, d.gx, d.gy, hx, ey, p.net, p.per_slice, a.dx, out);
   return hipGetLastError();
 }
 
@@ -632,7 +691,7 @@ hipError_t launch_router_logits(const void* x, const void* w, int router_f32, in
     if (E > 64 && blocks(128, 128) >= 192) return run_logits<128, 128, 2, 4, 4, true, 3>(x, w, T, H, E, z, st);
     if (E > 64 && blocks(64, 128) >= 192) return run_logits<64, 128, 2, 2, 4, true, 3>(x, w, T, H, E, z, st);
     if (blocks(64, 64) >= 192) return run_logits<64, 64, 2, 1, 4, true, 4>(x, w, T, H, E, z, st);
-    return run_logits<16, 32, 8, 1, 2, true, 3>(x, w, T, H, E, z, st);
+    return run_logits<32, 16, 8, 2, 1, true, 4>(x, w, T, H, E, z, st);
   }
   if (E > 64 && blocks(128, 128) >= 192) return run_logits<128, 128, 2, 4, 4, false, 4>(x, w, T, H, E, z, st);
   if (E > 64 && blocks(64, 128) >= 192) return run_logits<64, 128, 2, 2, 4, false, 4>(x, w, T, H, E, z, st);
@@ -656,27 +715,24 @@ hipError_t launch_router_backward(const RouterBackward& a, hipStream_t st) {
                        a.E, nw, p.net, wf, zf);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  if (a.dx) {
-    err = a.router_f32 ? run_dx<true>(a, wf, st) : run_dx<false>(a, wf, st);
-    if (err != hipSuccess) return err;
-  }
-  if (!a.dw) return err;
+  const DxPlan d = dx_plan(a.T, a.H, a.E);
   float* out = p.slices > 1 ? reinterpret_cast<float*>(a.ws + L.part) : a.dw;
-  const dim3 g((a.H + kDwH - 1) / kDwH, p.net / p.et, p.slices), b(kDwWaves * 64);
-  const uint16_t* x = static_cast<const uint16_t*>(a.x);
-  if (p.et == 8)
-    hipLaunchKernelGGL(router_dw_kernel<8>, g, b, 0, st, x, zf, a.T, a.H, a.E, p.net, p.per_slice,
-                       out);
-  else if (p.et == 4)
-    hipLaunchKernelGGL(router_dw_kernel<4>, g, b, 0, st, x, zf, a.T, a.H, a.E, p.net, p.per_slice,
-                       out);
-  else if (p.et == 2)
-    hipLaunchKernelGGL(router_dw_kernel<2>, g, b, 0, st, x, zf, a.T, a.H, a.E, p.net, p.per_slice,
-                       out);
-  else
-    hipLaunchKernelGGL(router_dw_kernel<1>, g, b, 0, st, x, zf, a.T, a.H, a.E, p.net, p.per_slice,
-                       out);
-  err = hipGetLastError();
+  if (a.dx && a.dw && d.ntl == 2 && p.et <= 2) {      // a short batch: both at once
+    if (p.et == 1) err = a.router_f32 ? run_both<1, true>(a, d, p, wf, zf, out, st)
+                                      : run_both<1, false>(a, d, p, wf, zf, out, st);
+    else err = a.router_f32 ? run_both<2, true>(a, d, p, wf, zf, out, st)
+                            : run_both<2, false>(a, d, p, wf, zf, out, st);
+  } else {
+    if (a.dx) {
+      err = a.router_f32 ? run_dx<true>(a, d, wf, st) : run_dx<false>(a, d, wf, st);
+      if (err != hipSuccess) return err;
+    }
+    if (!a.dw) return err;
+    err = p.et == 8   ? run_dw<8>(a, p, zf, out, st)
+          : p.et == 4 ? run_dw<4>(a, p, zf, out, st)
+          : p.et == 2 ? run_dw<2>(a, p, zf, out, st)
+                      : run_dw<1>(a, p, zf, out, st);
+  }
   if (err != hipSuccess || p.slices == 1) return err;
   const int64_t n4 = (int64_t)a.E * a.H / 4;
   hipLaunchKernelGGL(sum_slices_kernel, dim3((unsigned)((n4 + 255) / 256)), dim3(256), 0, st,
