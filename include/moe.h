@@ -167,7 +167,9 @@ int moe_route(const moe_desc* desc, const void* x, const void* w_router,
 
 /* moe_router_logits: logits[t][e] = sum over h of x[t][h] w_router[e][h], fp32
  * accumulation.  x device [T][H] BF16, w_router device [E][H] in
- * desc->router_wtype, logits device out [T][E] float; all 16-byte aligned. */
+ * desc->router_wtype, logits device out [T][E] float; all 16-byte aligned,
+ * logits apart from the others.  An infinity in x or an fp32 w_router may count
+ * as NaN. */
 int moe_router_logits(const moe_desc* desc, const void* x, const void* w_router,
                       int32_t T, float* logits, void* stream);
 
@@ -221,6 +223,8 @@ int moe_gate_backward(const moe_desc* desc, const float* logits, int32_t T,
  *   dx        device out [T][H] BF16 or NULL
  *   dw_router device out [E][H] float or NULL, overwritten
  *   ws        moe_workspace_bytes(.., MOE_MODE_ROUTER_BACKWARD)
+ * The outputs must not overlap each other or the inputs.  An infinity counts as
+ * NaN.
  * All 16-byte aligned.  0 <= T <= 2^20 (T == 0: dw_router is set to 0). */
 int moe_router_backward(const moe_desc* desc, const void* x, const void* w_router,
                         int32_t T, const float* dlogits, void* dx,
@@ -249,8 +253,11 @@ int moe_router_backward(const moe_desc* desc, const void* x, const void* w_route
  * it) and each row's gate-weighted result is added into y with an fp32
  * atomic, so the summation order (and the last bits of y) can differ
  * between runs.  INT4 experts: x as given, h in fp32 (handed on as three BF16
- * parts), fp32 accumulation, all T tokens in one pass, the sums in a fixed order
- * (no atomics on y, no wait between workgroups).
+ * parts), fp32 accumulation, all T tokens in one pass, no wait between
+ * workgroups, and equal calls give equal bits: at most two workgroups add into
+ * an element of y, which is cleared first (0 + a + b).  x is taken to be below
+ * 2^120 in magnitude; an infinity in it, or an h that overflows, makes the
+ * token's y NaN.
  *   x              device [T][H] BF16;   1 <= T <= MOE_DECODE_MAX_T
  *   ids, w         device [T][k] (from moe_route or the caller)
  *   slot_of_expert device [E] int32: slot holding expert e, -1 = not
@@ -415,7 +422,8 @@ int moe_q4_layout(const moe_q4_desc* desc, size_t offsets[3], size_t* bytes);
  * without zero points scale = max|v| / 7; with them scale = (hi - lo) / 15
  * with hi = max(v, 0), lo = min(v, 0), zero = -lo / scale rounded.  The scale
  * is rounded to BF16, then q = v / scale + zero rounded to the nearest (ties
- * to even) and clamped to 0..15. */
+ * to even) and clamped to 0..15.  The values are taken to be finite, with
+ * has_zero below 2^126 in magnitude. */
 int moe_q4_quantize(const moe_q4_desc* desc, const void* src, int32_t src_type,
                     int64_t src_ld, void* dst, void* stream);
 

@@ -105,6 +105,12 @@ Q4DecodeWs q4_decode_ws(const moe_desc* d, int T) {
 
 constexpr int kMaxGradTokens = 1 << 20;   // moe_router_backward
 
+// whether an output shares bytes with an input (either may be null)
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t p = (uintptr_t)a, q = (uintptr_t)b;
+  return a && b && p < q + nb && q < p + na;
+}
+
 struct GateWs {
   size_t ticket, share, n, s, c, total;
 };
@@ -608,6 +614,15 @@ int moe_router_backward(const moe_desc* desc, const void* x, const void* w_route
   if (!ws || ws_bytes < need || !aligned(ws, 256))
     return set_error(MOE_EWORKSPACE, "router backward workspace %zu < %zu bytes (or not "
                      "256-aligned)", ws_bytes, need);
+  // dx and dw_router may be written at the same time, while the inputs are read
+  const size_t nx = (size_t)T * desc->hidden * 2, nz = (size_t)T * desc->n_experts * 4;
+  const size_t nw = (size_t)desc->n_experts * desc->hidden;
+  const size_t nr = nw * (desc->router_wtype == MOE_WTYPE_F32 ? 4 : 2);
+  if (overlap(dx, nx, dw_router, nw * 4) || overlap(dx, nx, x, nx) ||
+      overlap(dx, nx, dlogits, nz) || overlap(dx, nx, w_router, nr) ||
+      overlap(dw_router, nw * 4, x, nx) || overlap(dw_router, nw * 4, dlogits, nz) ||
+      overlap(dw_router, nw * 4, w_router, nr))
+    return set_error(MOE_EINVAL, "dx and dw_router must not overlap each other or the inputs");
   moe::RouterBackward a;
   a.x = x; a.w = w_router; a.dz = dlogits; a.router_f32 = desc->router_wtype == MOE_WTYPE_F32;
   a.T = T; a.H = desc->hidden; a.E = desc->n_experts;

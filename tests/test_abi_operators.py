@@ -153,6 +153,25 @@ def test_router_calls(L):
     assert L.moe_workspace_bytes(_desc(), 0, 3) > 0
 
 
+def test_router_gradients_that_overlap(L):
+    """Each output against each of the others, by one byte at either end."""
+    d = _desc()
+    T, H, E = 64, d._obj.hidden, d._obj.n_experts
+    size = dict(x=T * H * 2, w=E * H * 2, dz=T * E * 4, dx=T * H * 2, dw=E * H * 4)
+    at = {n: (i + 1) << 32 for i, n in enumerate(size)}
+    need = L.moe_workspace_bytes(d, T, 4)
+
+    def call(p):
+        return L.moe_router_backward(d, p["x"], p["w"], T, p["dz"], p["dx"], p["dw"], 1 << 40,
+                                     need, None)
+    for out in ("dx", "dw"):
+        for other in size:
+            if other != out:
+                assert call({**at, out: at[other]}) == EINVAL
+                assert call({**at, out: at[other] + size[other] - 16}) == EINVAL
+                assert call({**at, out: at[other] - size[out] + 16}) == EINVAL
+
+
 def test_python_checks_name_the_argument():
     d = ops.make_desc(256, 128, 8, 2)
     x = torch.zeros((3, 256), dtype=torch.bfloat16)
