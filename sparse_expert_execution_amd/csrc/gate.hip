@@ -20,7 +20,7 @@
 namespace moe {
 namespace {
 
-constexpr int kGateWaves = 4;     // of the gradient
+constexpr int kGateWaves = 4;     // of the gradient's workgroup
 
 // e^x for x <= 0 as 2^(x log2 e): the product's rounding error and the constant's
 // are put back (without them the error grows with |x|)
@@ -68,6 +68,11 @@ __device__ __forceinline__ uint32_t row_min_u32(uint32_t v) {
 // Statistics: choices are counted in LDS (integers: any order); the sums of p
 // stay in registers over a wave's tokens and are added over its rows, then over
 // the workgroup's waves, in a fixed order: one partial row per workgroup.
+//
+// Bound by its vector instructions: a round looks at each of a lane's keys twice,
+// 2 k E operations a token.  T = 16384, E = 256, k = 8: 12.3 us against 3.4 us of
+// bytes; T = 200, E = 128: 6.0 us, nearly all of it latency (4 waves a workgroup
+// instead of 16: the same).
 template <int C, int WAVES, int KB, bool STATS>
 __global__ __launch_bounds__(WAVES * 64) void gate_kernel(GateArgs a) {
   constexpr int V = 4 * C;                            // logits per lane
@@ -78,7 +83,7 @@ __global__ __launch_bounds__(WAVES * 64) void gate_kernel(GateArgs a) {
     for (int i = threadIdx.x; i <= C * 64; i += WAVES * 64) lc[i] = 0;
     __syncthreads();
   }
-  const bool vec = a.E % 4 == 0;
+  const bool vec = a.E % 4 == 0 && (uintptr_t)a.z % 16 == 0;
   float S[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) S[i] = 0.f;
@@ -201,8 +206,8 @@ __global__ __launch_bounds__(WAVES * 64) void gate_kernel(GateArgs a) {
 
 // Partial rows -> counts and the loss.  A workgroup takes 16 experts, 64 threads
 // of each every 64th row; the last workgroup to finish adds the workgroups' shares
-// of the loss in order.  (64 experts a workgroup, four times the bytes for each
-// compute unit, took 4.1 us for 256 rows of 256 experts.)
+// of the loss in order.  Bound by latency: 3.9 us for 256 rows of 256 experts (64
+// experts a workgroup: 4.1), 4 us for 13 rows of 128 (one workgroup for all: 5.2).
 constexpr int kReduceExperts = 16, kReduceSlices = 64;
 
 __global__ __launch_bounds__(kReduceExperts * kReduceSlices) void gate_reduce_kernel(GateArgs a,
@@ -272,12 +277,14 @@ __global__ __launch_bounds__(kReduceExperts * kReduceSlices) void gate_reduce_ke
 // Four tokens per wave, as in gate_kernel; lane j of a row holds the token's
 // choices j, j + 16, ..  Their terms meet the others in LDS: a comparison of each
 // of a lane's experts with each choice cost more than the rest together.
+// Bound by HBM and, at this size, by the launch: T = 16001, E = 256, k = 8 11.8 us,
+// 2.9 TB/s (6.6 us at the rate of a long copy).
 template <int C, int KB>
 __global__ __launch_bounds__(kGateWaves * 64) void gate_backward_kernel(GateBackward a) {
   constexpr int V = 4 * C;
   __shared__ v4f s_dz[kGateWaves][4][C * 16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane & 15, row = lane >> 4;
-  const bool vec = a.E % 4 == 0;
+  const bool vec = a.E % 4 == 0 && ((uintptr_t)a.z | (uintptr_t)a.dz) % 16 == 0;
   float p[V], w[KB], dw[KB], b[V];
   int id[KB];
   auto load = [&](int64_t t) {
@@ -425,7 +432,7 @@ hipError_t launch_gate(const GateArgs& a, hipStream_t st) {
 template <int C>
 hipError_t run_backward(const GateBackward& a, hipStream_t st) {
   // four tokens a wave, up to eight waves a SIMD
-  const int quads = (a.T + 3) / 4, most = 8192;
+  const int quads = (a.T - 1) / 4 + 1, most = 8192;     // T >= 1, up to 2^31 - 1
   const dim3 g(((quads < most ? quads : most) + kGateWaves - 1) / kGateWaves), b(kGateWaves * 64);
   if (a.k <= 16) hipLaunchKernelGGL((gate_backward_kernel<C, 1>), g, b, 0, st, a);
   else hipLaunchKernelGGL((gate_backward_kernel<C, 4>), g, b, 0, st, a);

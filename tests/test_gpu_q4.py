@@ -288,7 +288,7 @@ def _oracle(L, x, ids, w, include=None):
 
 # h carries the gate/up product's error (under 5e-6 of the norm; SwiGLU at most
 # doubles a relative error of values of order one, twice for the product) and
-# the two-part split's 2^-18; the down product adds its own: 4e-5 in all
+# the split of h, at most 2^-18; the down product adds its own: 4e-5 in all
 EXPERT_TOL = 4e-5
 
 EXPERTS = [
@@ -407,7 +407,7 @@ def test_experts_in_a_graph_beside_eager_calls(ops):
 def test_experts_in_a_pool_that_fills_its_allocation(ops):
     """The last expert's blocks end with the pool (153 pages of 2 MiB): the loads
     that run ahead of the last job stay inside it.  Bytes are random codes under a
-    scale of 1 (BF16 0x3F80) by construction of the sections."""
+    scale of 2^-10 (BF16 0x3A80) by construction of the sections."""
     H, I, E, k, T = 2048, 768, 128, 8, 64
     desc = ops.make_desc(H, I, E, k, wtype="int4_g64")
     off, n = ops.expert_layout(desc)
@@ -430,6 +430,77 @@ def test_experts_in_a_pool_that_fills_its_allocation(ops):
         torch.cuda.synchronize()
         ys.append(y)
     assert torch.isfinite(ys[0]).all() and torch.equal(ys[0], ys[1]) and torch.equal(ys[0], ys[2])
+
+
+def test_experts_of_a_large_layer_in_far_slots(ops):
+    """1024 experts, more pairs than one wave lists, slots past 4 GiB of the pool.
+    Every expert holds one of four blocks, so that a small layer of these four is
+    the oracle."""
+    H, I, E, k, T, far = 256, 1536, 1024, 8, 64, 8000
+    L = _Layer(ops, H, I, 4, 4, 128, True, seed=21)
+    blocks = L.pool.view(4, L.bytes)
+    assert far * L.bytes > 1 << 32
+    desc = ops.make_desc(H, I, E, k, has_shared=True, wtype="int4_g128")
+    assert ops.expert_layout(desc)[1] == L.bytes
+    pool = torch.zeros((far + E, L.bytes), dtype=torch.uint8, device="cuda")
+    slots = L.rng.permutation(E) + np.where(np.arange(E) % 2, far, 0)
+    slot_of = torch.from_numpy(slots.astype(np.int32)).cuda()
+    for m in range(4):
+        pool[slot_of[m::4].long()] = blocks[m]
+    x = torch.from_numpy(L.rng.standard_normal((T, H)).astype(np.float32)).to(
+        torch.bfloat16).cuda()
+    ids = np.stack([L.rng.choice(E, k, replace=False) for _ in range(T)]).astype(np.int32)
+    w = L.rng.uniform(0.05, 0.4, (T, k)).astype(np.float32)
+    y = torch.full((T, H), float("nan"), device="cuda")
+    ops.decode(desc, x, torch.from_numpy(ids).cuda(), torch.from_numpy(w).cuda(), pool.view(-1), y,
+               ops.workspace(desc, T, ops.MODE_DECODE), slot_of=slot_of, shared=L.shared)
+    torch.cuda.synchronize()
+    small = np.zeros((T, 4))
+    np.add.at(small, (np.arange(T)[:, None], ids % 4), w.astype(np.float64))
+    ref = _oracle(L, x, np.tile(np.arange(4, dtype=np.int32), (T, 1)), small)
+    y = y.cpu().numpy()
+    assert np.linalg.norm(y - ref) <= EXPERT_TOL * np.linalg.norm(ref)
+    assert olayer.row_rel_error(y, ref) < 10 * EXPERT_TOL
+
+
+def test_experts_tokens_do_not_mix(ops):
+    """A padded batch: a token of NaN or infinities stays in its row, also where it
+    shares its experts with others."""
+    L = _Layer(ops, 256, 128, 4, 2, 32, True, seed=22)
+    x, ids, w = L.inputs(21)
+    clean = _run(ops, L, x, ids, w)
+    bad = x.clone()
+    bad[3] = float("nan")
+    bad[20, 7] = float("inf")
+    y = _run(ops, L, bad, ids, w)
+    keep = np.setdiff1d(np.arange(21), [3, 20])
+    assert np.array_equal(y[keep], clean[keep])
+    assert np.all(np.isnan(y[3])) and np.all(np.isnan(y[20]))
+
+
+def test_linear_past_four_gibibytes(ops):
+    """The last rows of a matrix whose codes pass 32 bits, against a matrix of
+    these rows alone (bytes of theirs, in a block of their own)."""
+    N, K, group, last = 131072, 66048, 128, 32
+    desc, part = ops.make_q4(N, K, group=group), ops.make_q4(last, K, group=group)
+    off, n = ops.q4_layout(desc)
+    assert off[1] > 1 << 32
+    q, s, z = _matrix(np.random.default_rng(23), last, K, group, False)
+    small = _pack(ops, part, q, s, z)
+    codes = ops.q4_layout(part)[0][1]
+    block = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    block[off[1] - codes:off[1]] = small[:codes]
+    block[n - (small.numel() - codes):] = small[codes:]
+    for T in (1, 6):
+        x = torch.from_numpy(np.random.default_rng(T).standard_normal((T, K)).astype(
+            np.float32)).to(torch.bfloat16).cuda()
+        y = torch.full((T, N), float("nan"), device="cuda")
+        ops.q4_linear(desc, x, block, y)
+        torch.cuda.synchronize()
+        xo = bf16_to_f64(x)
+        assert torch.all(y[:, :N - last] == 0)
+        _check(y[:, N - last:].cpu().numpy(), xo @ oq4.decode(q, s, z, group).T,
+               _bound(xo, q, s, z, group))
 
 
 def test_experts_from_the_cache(ops):

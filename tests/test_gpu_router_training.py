@@ -129,6 +129,31 @@ def test_gate_backward(ops, T, E, k, renorm, masked, which):
     assert torch.equal(zd, dz[:T])
 
 
+@pytest.mark.parametrize("E", [128, 20])
+def test_gate_on_unaligned_logits(ops, E):
+    """Logits and their gradient that start at any element."""
+    T, k = 50, 4
+    z, _, rng = _logits(T, E, 31)
+    desc, zd, ids, w, counts, loss = _gate(ops, z, k)
+    dw = torch.from_numpy(rng.standard_normal((T, k)).astype(np.float32)).cuda()
+    one = torch.ones(1, device="cuda")
+    dz = torch.empty((T, E), device="cuda")
+    ops.gate_backward(desc, zd, ids, w, dz, dw=dw, counts=counts, dloss=one)
+    ws = ops.workspace(desc, T, ops.MODE_GATE)
+    for shift in (1, 2, 3):
+        buf = torch.full((2, shift + T * E + 1), -7.0, device="cuda")
+        z2, dz2 = (b[shift:shift + T * E].view(T, E) for b in buf)
+        z2.copy_(zd)
+        ids2, w2, counts2 = torch.empty_like(ids), torch.empty_like(w), torch.empty_like(counts)
+        loss2 = torch.empty_like(loss)
+        ops.gate(desc, z2, ids2, w2, ws, counts=counts2, loss=loss2)
+        ops.gate_backward(desc, z2, ids2, w2, dz2, dw=dw, counts=counts2, dloss=one)
+        torch.cuda.synchronize()
+        for a, b in ((ids, ids2), (w, w2), (counts, counts2), (loss, loss2), (dz, dz2)):
+            assert torch.equal(a, b)
+        assert torch.all(buf[:, :shift] == -7) and torch.all(buf[:, -1] == -7)
+
+
 def test_gate_ties_and_signed_zeros(ops):
     z = np.zeros((4, 70), dtype=np.float32)
     z[1, ::2] = -0.0
@@ -205,6 +230,9 @@ ROUTER = [
     (2048, 64, 20, "bf16"),
     (12289, 96, 200, "bf16"), (12289, 160, 256, "f32"), (12300, 64, 100, "f32"),
     (12300, 96, 101, "bf16"), (12300, 32, 40, "f32"), (12300, 224, 64, "bf16"),
+    # dx and dW in one launch, with one and with two expert tiles of dW a workgroup
+    (1000, 2048, 256, "f32"), (1000, 2048, 256, "bf16"), (500, 1024, 96, "bf16"),
+    (1 << 20, 32, 3, "bf16"),                      # the most tokens
 ]
 
 
