@@ -70,7 +70,7 @@ __device__ __forceinline__ uint32_t row_min_u32(uint32_t v) {
 // the workgroup's waves, in a fixed order: one partial row per workgroup.
 //
 // Bound by its vector instructions: a round looks at each of a lane's keys twice,
-// 2 k E operations a token.  T = 16384, E = 256, k = 8: 12.3 us against 3.4 us of
+// 2 k E operations a token.  T = 16384, E = 256, k = 6: 12.3 us against 3.4 us of
 // bytes; T = 200, E = 128: 6.0 us, nearly all of it latency (4 waves a workgroup
 // instead of 16: the same).
 template <int C, int WAVES, int KB, bool STATS>
@@ -264,9 +264,9 @@ __global__ __launch_bounds__(kReduceExperts * kReduceSlices) void gate_reduce_ke
   }
   if (!__builtin_amdgcn_readfirstlane(last)) return;
   // at most 64 workgroups (1024 experts): a lane each, added in a fixed order
-  const float v = lane < (int)gridDim.x
-                      ? __hip_atomic_load(&a.share[lane], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)
-                      : 0.f;
+  float v = 0.f;
+  if (lane < (int)gridDim.x)
+    v = __hip_atomic_load(&a.share[lane], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   const float total = wave_sum_dpp(v);
   if (lane == 0) {
     const float d = (float)a.k * (float)n * (float)n;
@@ -277,7 +277,7 @@ __global__ __launch_bounds__(kReduceExperts * kReduceSlices) void gate_reduce_ke
 // Four tokens per wave, as in gate_kernel; lane j of a row holds the token's
 // choices j, j + 16, ..  Their terms meet the others in LDS: a comparison of each
 // of a lane's experts with each choice cost more than the rest together.
-// Bound by HBM and, at this size, by the launch: T = 16001, E = 256, k = 8 11.8 us,
+// Bound by HBM and, at this size, by the launch: T = 16001, E = 256, k = 6 11.8 us,
 // 2.9 TB/s (6.6 us at the rate of a long copy).
 template <int C, int KB>
 __global__ __launch_bounds__(kGateWaves * 64) void gate_backward_kernel(GateBackward a) {
@@ -431,8 +431,8 @@ hipError_t launch_gate(const GateArgs& a, hipStream_t st) {
 
 template <int C>
 hipError_t run_backward(const GateBackward& a, hipStream_t st) {
-  // four tokens a wave, up to eight waves a SIMD
-  const int quads = (a.T - 1) / 4 + 1, most = 8192;     // T >= 1, up to 2^31 - 1
+  // four tokens a wave, up to eight waves a SIMD (T >= 1, up to 2^31 - 1)
+  const int quads = (a.T - 1) / 4 + 1, most = 8192;
   const dim3 g(((quads < most ? quads : most) + kGateWaves - 1) / kGateWaves), b(kGateWaves * 64);
   if (a.k <= 16) hipLaunchKernelGGL((gate_backward_kernel<C, 1>), g, b, 0, st, a);
   else hipLaunchKernelGGL((gate_backward_kernel<C, 4>), g, b, 0, st, a);

@@ -19,6 +19,11 @@ constexpr int kWaves = 8;
 // 128 columns at a time and each wave for itself: loads run along the rows (16
 // lanes x 16 bytes), piece p of row i is kept at slot p ^ i % 16, from where the
 // operand is read without bank conflicts.
+//
+// Bound: HBM for large matrices, 131072 x 4096 and one token 53 us, 5.2 TB/s; the
+// launch for small ones, 768 x 2048 and one token 3.4 us of kernel in 5.4 us a
+// call.  With more tokens the operands' way through the L1 and LDS: 8192 x 4096
+// (groups of 128) 16 tokens 6.5 us, 32 9.4 us, 64 13.3 us.
 template <int NT, int TI, int RT, int G, bool ZERO, bool STAGE>
 __global__ __launch_bounds__(kWaves * 64, NT > 1 ? 2 : 4) void
 q4_linear_kernel(Q4Linear a) {

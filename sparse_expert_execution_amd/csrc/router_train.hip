@@ -64,6 +64,10 @@ __device__ __forceinline__ void split8x3(const float (&v)[8], u32x4& hi, u32x4& 
 // experts is expert 4 WE q + 4 j + i, so a lane stores 4 WE consecutive ones.
 // An fp32 W is split into three BF16 parts in registers (all 24 bits; BF16
 // products are exact, so z is an fp32 sum of exact terms).
+//
+// Bound: for long batches the loads into the compute units (see
+// launch_router_logits), twice the time of the matrix instructions; for short
+// ones latency.
 constexpr int kLgWaves = 8;
 
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
@@ -149,7 +153,8 @@ __global__ __launch_bounds__(kLgWaves * 64) void router_logits_kernel(
     // copies 0..kX-1 are x, the rest W, 64 pieces each
     const bool is_x = i < kX;
     const int n = (is_x ? i : i - kX) * 64 + lane, np = is_x ? NPX : NPW;
-    const int row = n / np, p = is_x ? piece_slot<NPX>(row, n % NPX) : piece_slot<NPW>(row, n % NPW);
+    const int row = n / np;
+    const int p = is_x ? piece_slot<NPX>(row, n % NPX) : piece_slot<NPW>(row, n % NPW);
     if (is_x) {
       const int64_t t = t0 + row < T ? t0 + row : T - 1;
       src[c] = reinterpret_cast<const uint8_t*>(x + t * H);
@@ -276,7 +281,7 @@ __global__ __launch_bounds__(kLgWaves * 64) void router_logits_kernel(
 template <int TM, int TE, int KS, int WT, int WE, bool RF32, int STAGES>
 hipError_t run_logits(const void* x, const void* w, int T, int H, int E, float* z,
                       hipStream_t st) {
-  const dim3 g((T + TM - 1) / TM, (E + TE - 1) / TE);
+  const dim3 g((T - 1) / TM + 1, (E + TE - 1) / TE);   // T >= 1, up to 2^31 - 1
   constexpr size_t lds = (size_t)STAGES * (TM * 4 + TE * (RF32 ? 8 : 4)) * KS * 16;
   hipLaunchKernelGGL((router_logits_kernel<TM, TE, KS, WT, WE, RF32, STAGES>), g,
                      dim3(kLgWaves * 64), lds, st, static_cast<const uint16_t*>(x), w, T, H, E, z);
@@ -287,7 +292,9 @@ hipError_t run_logits(const void* x, const void* w, int T, int H, int E, float* 
 // W for dx: [chunk of 64 h][32 e][tile j][part][64 lanes]; dz^T for dW:
 // [32 tokens][16 e][part][64 lanes], three parts of it (dW is fp32: with two its
 // error was 2.5e-6 of its norm where an fp32 product has 5e-7).  One launch for
-// both: workgroups 0 .. nw - 1 take W, the others dz.
+// both: workgroups 0 .. nw - 1 take W, the others dz.  Bound: HBM and latency;
+// 10 us at T = 16384, H = 4096, E = 256, 3.5 us at 777, 2048, 128 (two launches
+// were 3 us more).
 constexpr int kZp = 3;
 
 template <bool RF32>
@@ -347,7 +354,11 @@ __global__ __launch_bounds__(256) void pack_kernel(const void* __restrict__ w,
 
 // ---- dx -----------------------------------------------------------------------
 // A workgroup holds dz of 16 NTL tokens (all experts, both parts, operand
-// order) in LDS, and its 8 waves stream chunks of 64 h of W past it.
+// order) in LDS, and its 8 waves stream chunks of 64 h of W past it: W, the
+// operand without reuse in a workgroup, comes from the L2 in operand order.
+//
+// Bound: the matrix cores, 2 T H E operations for each part of dz (three pairs of
+// parts where W is fp32).  T = 16384, H = 4096, E = 256: 75 us, 0.92 PFLOP/s.
 constexpr int kDxWaves = 8;
 
 template <int NTL, bool RF32>
@@ -456,6 +467,9 @@ __device__ __forceinline__ void router_dx(const float* __restrict__ dz,
 // has 64 h of its own, whose x it reads straight from memory (lane (n, q): 8
 // tokens x 4 h) and transposes in registers: column n of the f-th operand is
 // h = 4 n + f, so a lane ends up with four consecutive h of a row.
+//
+// Bound: the matrix cores, three times 2 T H E operations.  T = 16384, H = 4096, E
+// = 256: 96 us, 1.07 PFLOP/s, and 11 us for the sum over 16 slices of tokens.
 constexpr int kDwWaves = 8, kDwH = 64 * kDwWaves;
 
 __device__ __forceinline__ uint32_t pack_lo(uint32_t a, uint32_t b) {
@@ -563,7 +577,8 @@ __global__ __launch_bounds__(kDwWaves * 64, 2) void router_dw_kernel(const uint1
 }
 
 // Both in one launch, where neither fills the chip: workgroups 0 .. ndx - 1 are
-// dx's (gx of them side by side), the others dW's.
+// dx's (gx of them side by side), the others dW's.  T = 777, H = 2048, E = 128, W
+// fp32: 11.7 us, one after the other 8.1 + 7.8.
 template <int ET, bool RF32>
 __global__ __launch_bounds__(kDxWaves * 64, 2) void router_both_kernel(
     const uint16_t* x, const float* dz, const u32x4* wf, const u32x4* zf, int T, int H, int E,
@@ -682,19 +697,25 @@ hipError_t launch_router_logits(const void* x, const void* w, int router_f32, in
   // A compute unit takes in about 40 GB/s through its L1 here (its misses in
   // flight over the L2's latency), so the tile with the fewest bytes per result
   // that still gives 192 workgroups (3/4 of the compute units) is the fastest:
-  // 128 x 128 before 64 x 128 before 64 x 64; last 16 x 32, where a workgroup's
-  // waves all split H.  T = 16384, H = 4096, E = 256: 64 x 256 tiles 63 us.
+  // 128 x 128 before 64 x 128 before 64 x 64; last tiles whose waves all split H:
+  // 16 x 32, and 32 x 16 where W is fp32 (a row of it is as many bytes as two of
+  // x).  T = 16384, H = 4096, E = 256: 128 x 128 tiles 60 us (0.57 PFLOP/s), 64 x
+  // 256 63 us; T = 777, H = 2048, E = 128, W fp32: 32 x 16 10.3 us, 16 x 32 11.2.
   const auto blocks = [&](int tokens, int experts) {
-    return (int64_t)((T + tokens - 1) / tokens) * ((E + experts - 1) / experts);
+    return (int64_t)((T - 1) / tokens + 1) * ((E + experts - 1) / experts);
   };
   if (router_f32) {
-    if (E > 64 && blocks(128, 128) >= 192) return run_logits<128, 128, 2, 4, 4, true, 3>(x, w, T, H, E, z, st);
-    if (E > 64 && blocks(64, 128) >= 192) return run_logits<64, 128, 2, 2, 4, true, 3>(x, w, T, H, E, z, st);
+    if (E > 64 && blocks(128, 128) >= 192)
+      return run_logits<128, 128, 2, 4, 4, true, 3>(x, w, T, H, E, z, st);
+    if (E > 64 && blocks(64, 128) >= 192)
+      return run_logits<64, 128, 2, 2, 4, true, 3>(x, w, T, H, E, z, st);
     if (blocks(64, 64) >= 192) return run_logits<64, 64, 2, 1, 4, true, 4>(x, w, T, H, E, z, st);
     return run_logits<32, 16, 8, 2, 1, true, 4>(x, w, T, H, E, z, st);
   }
-  if (E > 64 && blocks(128, 128) >= 192) return run_logits<128, 128, 2, 4, 4, false, 4>(x, w, T, H, E, z, st);
-  if (E > 64 && blocks(64, 128) >= 192) return run_logits<64, 128, 2, 2, 4, false, 4>(x, w, T, H, E, z, st);
+  if (E > 64 && blocks(128, 128) >= 192)
+    return run_logits<128, 128, 2, 4, 4, false, 4>(x, w, T, H, E, z, st);
+  if (E > 64 && blocks(64, 128) >= 192)
+    return run_logits<64, 128, 2, 2, 4, false, 4>(x, w, T, H, E, z, st);
   if (blocks(64, 64) >= 192) return run_logits<64, 64, 2, 1, 4, false, 4>(x, w, T, H, E, z, st);
   return run_logits<16, 32, 8, 1, 2, false, 4>(x, w, T, H, E, z, st);
 }
