@@ -98,7 +98,7 @@ Q4DecodeWs q4_decode_ws(const moe_desc* d, int T) {
   w.n_units = o; o = align_up(o + 4);
   w.units = o; o = align_up(o + (P + 1) * 16);
   w.entries = o; o = align_up(o + (P + T) * 2);
-  w.h = o; o = align_up(o + (P + T) * d->inter * 8);
+  w.h = o; o = align_up(o + (P + T) * d->inter * 6);
   w.total = o;
   return w;
 }
@@ -210,7 +210,7 @@ static int q4_decode_impl(const moe_desc* desc, const void* x, const void* w_rou
                           size_t ws_bytes, void* stream) {
   // the kernels address the rows of x and h by 32-bit byte offsets
   if ((int64_t)T * desc->hidden * 2 >= (int64_t)1 << 31 ||
-      (int64_t)T * (desc->top_k + 1) * desc->inter * 8 >= (int64_t)1 << 31)
+      (int64_t)T * (desc->top_k + 1) * desc->inter * 6 >= (int64_t)1 << 31)
     return set_error(MOE_EUNSUPPORTED, "decode shape H=%d I=%d too wide for %d tokens",
                      desc->hidden, desc->inter, T);
   const Q4DecodeWs L = q4_decode_ws(desc, T);

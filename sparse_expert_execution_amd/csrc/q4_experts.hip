@@ -190,10 +190,10 @@ __device__ __forceinline__ void gate_up_columns(const Q4Experts& a, const uint8_
     if (col >= n_cols) continue;
     const float h = g / (1.f + expf(-g)) * u;
     // h as three BF16 parts, all 24 bits of it: y keeps fp32's accuracy rather
-    // than BF16's.  Laid out [entry][32 of I][8 of I][part, 4][8], as four
+    // than BF16's.  Laid out [entry][8 of I][part][8], as four
     // neighbouring lanes of the down product read it.
     const int row = 16 * tile + (l & 15);
-    const int64_t at = (int64_t)entries[col] * a.I * 4 + (row >> 3) * 32 + (row & 7);
+    const int64_t at = (int64_t)entries[col] * a.I * 3 + (row >> 3) * 24 + (row & 7);
     const __bf16 h0 = (__bf16)h;
     const float r1 = h - (float)h0;
     const __bf16 h1 = (__bf16)r1;
@@ -324,7 +324,7 @@ __global__ __launch_bounds__(kDnWaves * 64, 4) void q4_down_kernel(Q4Experts a, 
   const int job0 = uni(wave) * gridDim.y + blockIdx.y;
   int ii = uni(job0 / slices), sl = uni(job0 - ii * slices);
   int kb = 0, kend = 0, first = 0, count = 0, slot = 0;
-  const Buffer hb = buffer_of(a.h, (uint32_t)(a.P + a.T) * a.I * 8);
+  const Buffer hb = buffer_of(a.h, (uint32_t)(a.P + a.T) * a.I * 6);
   uint32_t hrow = kNowhere;                           // bytes
   auto start = [&]() {
     const int item = uni(s_item[ii]), c0 = item & 1023;
@@ -335,7 +335,7 @@ __global__ __launch_bounds__(kDnWaves * 64, 4) void q4_down_kernel(Q4Experts a, 
     kb = sl * per;
     kend = min(kb + per, nkb);
     hrow = part < 3 && e4 < count
-               ? (uint32_t)entries[first + e4] * a.I * 8 + q * 64 + part * 16
+               ? (uint32_t)entries[first + e4] * a.I * 6 + q * 48 + part * 16
                : kNowhere;
   };
 
@@ -353,7 +353,7 @@ __global__ __launch_bounds__(kDnWaves * 64, 4) void q4_down_kernel(Q4Experts a, 
     const uint8_t* block = slot < 0 ? a.shared : a.pool + (int64_t)uni(slot) * a.expert_bytes;
     const Matrix m{block + a.off[4], block + a.off[5], nullptr, nkb};
     load_tile<G, false>(b.t[0], m, tile, kb, in);
-    load_rows<256>(b.x[0], hb, hrow, 1024 * kb, in ? a.I - 128 * kb : 0);
+    load_rows<192>(b.x[0], hb, hrow, 768 * kb, in ? a.I - 128 * kb : 0);
     b.flush = 0;
     b.at = first;
     if (!in) return;
