@@ -60,14 +60,37 @@ __device__ __forceinline__ bf16x8 minus_16_plus(uint32_t z) {
 __device__ __forceinline__ int slot_token(int r) { return (r >> 2) + 4 * (r & 3); }
 __device__ __forceinline__ int result_token(int lane, int i) { return (lane >> 4) + 4 * i; }
 
-// what a lane holds of one tile: its codes, and per group the scale (and zero
-// point) of its row
+// what a lane holds of one tile: its codes, and of group l / 16 % (128 / G) the
+// scale (and zero point) of its row
 template <int G, bool ZERO>
 struct Tile {
   uint4 codes;
-  uint16_t scale[128 / G];
-  uint8_t zero[ZERO ? 128 / G : 1];
+  uint16_t scale;
+  uint8_t zero;
 };
+
+// v of lane group l / 16 % N -> the N groups' values in every lane.  One load of
+// all groups and these exchanges instead of a load per group: a load costs its 64
+// addresses whatever it brings.
+template <int N>
+__device__ __forceinline__ void spread(uint32_t v, uint32_t (&o)[N]) {
+  if constexpr (N == 1) {
+    o[0] = v;
+  } else if constexpr (N == 2) {
+    const auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    o[0] = p[0];
+    o[1] = p[1];
+  } else {
+    static_assert(N == 4, "groups of 32, 64 or 128");
+    const auto h = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    const auto a = __builtin_amdgcn_permlane16_swap(h[0], h[0], false, false);
+    const auto b = __builtin_amdgcn_permlane16_swap(h[1], h[1], false, false);
+    o[0] = a[0];
+    o[1] = a[1];
+    o[2] = b[0];
+    o[3] = b[1];
+  }
+}
 
 struct Matrix {
   const uint8_t* codes;     // [row tiles][column blocks][64 lanes][16]
@@ -88,11 +111,9 @@ __device__ __forceinline__ void load_tile(Tile<G, ZERO>& t, const Matrix& m, int
   t.codes = ldg16(codes + lane * 16);
   const uint8_t* scales = m.scales + at * (128 / G) * 32;
   const uint8_t* zeros = m.zeros + at * (128 / G) * 16;
-#pragma unroll
-  for (int g = 0; g < 128 / G; ++g) {
-    t.scale[g] = *reinterpret_cast<const uint16_t*>(scales + 32 * g + (lane & 15) * 2);
-    if (ZERO) t.zero[g] = zeros[16 * g + (lane & 15)];
-  }
+  const uint32_t i = lane & (16 * 128 / G - 1);
+  t.scale = *reinterpret_cast<const uint16_t*>(scales + i * 2);
+  if (ZERO) t.zero = zeros[i];
 }
 
 // A buffer of `bytes` bytes for loads whose lanes with nothing to read take an
@@ -129,6 +150,10 @@ template <int RT, int NT, int TI, int G, bool ZERO>
 __device__ __forceinline__ void mul_tiles(float (&acc)[RT][NT][TI], const Tile<G, ZERO> (&t)[RT],
                                           const bf16x8 (&x)[NT][4]) {
   constexpr int S = G / 32;
+  uint32_t sz[RT][128 / G];                           // scale, zero point above it
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+    spread(ZERO ? t[r].scale | (uint32_t)t[r].zero << 16 : t[r].scale, sz[r]);
 #pragma unroll
   for (int g = 0; g < 128 / G; ++g) {
     v4f c[NT];                                        // -24 sum x: for all tiles the same
@@ -146,8 +171,8 @@ __device__ __forceinline__ void mul_tiles(float (&acc)[RT][NT][TI], const Tile<G
       bf16x8 w[S], z;
 #pragma unroll
       for (int s = 0; s < S; ++s) w[s] = codes_plus16(dword(t[r].codes, g * S + s));
-      if (ZERO) z = minus_16_plus(t[r].zero[g]);
-      const float sc = __uint_as_float((uint32_t)t[r].scale[g] << 16);
+      if (ZERO) z = minus_16_plus(sz[r][g] >> 16);
+      const float sc = __uint_as_float(sz[r][g] << 16);
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         v4f d = ZERO ? v4f{0.f, 0.f, 0.f, 0.f} : c[j];
