@@ -114,20 +114,22 @@ __device__ __forceinline__ void wave_units(const Q4Experts& a, UnitList& u) {
 }
 
 // ---- gate / up --------------------------------------------------------------
-// grid (row tiles of I, units).  A workgroup's waves are four slices of H for one
-// row tile of both matrices; the partial sums meet in LDS in slice order.  x comes
-// from the L2 straight into the operand's registers.
+// grid (row tiles of I / per, units).  A workgroup's waves are four slices of H for
+// `per` row tiles of both matrices, one after the other; the partial sums meet in
+// LDS in slice order, while the next tile's loads are in flight.  x comes from the
+// L2 straight into the operand's registers.  (Eight waves for one token's few
+// workgroups: 7.4 us instead of 7.1.)
 //
 // Bound: HBM, 4 tokens with 6 experts each and a shared one, H = 4096, I = 2048,
 // groups of 32: 50 us, 4.6 TB/s; one token (2048/768, 8 experts) 7 us, latency; 64
-// tokens on the 128 experts of 2048/768, groups of 64: 55 us, 3.8 TB/s, the loads
+// tokens on the 128 experts of 2048/768, groups of 64: 51 us, 4.1 TB/s, the loads
 // of x (a cache access per lane) beside those of the experts.
 constexpr int kGuWaves = 4;
 
 template <int TI, int G>
-__device__ __forceinline__ void gate_up_columns(const Q4Experts& a, const uint8_t* block, int tile,
-                                                const int16_t* entries, int n_cols,
-                                                float (&red)[2][4][kGuWaves][64]) {
+__device__ __forceinline__ void gate_up_columns(const Q4Experts& a, const uint8_t* block, int tile0,
+                                                int tiles, const int16_t* entries, int n_cols,
+                                                float (&red)[2][2][4][kGuWaves][64]) {
   constexpr int D = 2;
   const int lane = threadIdx.x & 63, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -146,67 +148,91 @@ __device__ __forceinline__ void gate_up_columns(const Q4Experts& a, const uint8_
   struct Block {
     Tile<G, false> t[2];
     bf16x8 x[1][4];
+    int valid, flush;                                 // the last block of its row tile
   };
-  const int n_it = wave < nkb ? (nkb - wave + kGuWaves - 1) / kGuWaves : 0;
-  auto load = [&](Block& b, int it) {
-    const bool in = it < n_it;
-    const int kb = wave + (in ? it : 0) * kGuWaves;
-    load_tile<G, false>(b.t[0], mg, tile, kb, in);
-    load_tile<G, false>(b.t[1], mu, tile, kb, in);
-    load_rows<64>(b.x[0], xb, xrow, 256 * kb, in ? a.H - 128 * kb : 0);
+  // where the loads are: row tile `rt`, column block kb; past the last one the
+  // first again
+  int rt = wave < nkb ? 0 : tiles, kb = wave;
+  auto load = [&](Block& b) {
+    const bool in = rt < tiles;
+    const int k = in ? kb : 0, r = tile0 + (in ? rt : 0);
+    load_tile<G, false>(b.t[0], mg, r, k, in);
+    load_tile<G, false>(b.t[1], mu, r, k, in);
+    load_rows<64>(b.x[0], xb, xrow, 256 * k, in ? a.H - 128 * k : 0);
+    b.valid = in;
+    kb += kGuWaves;
+    b.flush = kb >= nkb;
+    if (b.flush) {
+      kb = wave;
+      ++rt;
+    }
   };
   float acc[2][1][TI];
+  int done = 0;
+  // a row tile's sums: every wave comes here once for each.  Two buffers: a wave
+  // writes one of them again only after a barrier behind which all have read it.
+  auto finish = [&]() {
+    const int buf = done & 1;
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+      red[buf][0][i][wave][lane] = acc[0][0][i];
+      red[buf][1][i][wave][lane] = acc[1][0][i];
+      acc[0][0][i] = acc[1][0][i] = 0.f;
+    }
+    __syncthreads();
+    for (int id = threadIdx.x; id < TI * 64; id += kGuWaves * 64) {
+      const int l = id & 63, i = id >> 6;
+      float g = 0.f, u = 0.f;
+#pragma unroll
+      for (int s = 0; s < kGuWaves; ++s) {
+        g += red[buf][0][i][s][l];
+        u += red[buf][1][i][s][l];
+      }
+      const int col = result_token(l, i);
+      if (col >= n_cols) continue;
+      const float h = g / (1.f + expf(-g)) * u;
+      // h as three BF16 parts, all 24 bits of it: y keeps fp32's accuracy rather
+      // than BF16's.  Laid out [entry][8 of I][part][8], as four neighbouring
+      // lanes of the down product read it.
+      const int row = 16 * (tile0 + done) + (l & 15);
+      const int64_t at = (int64_t)entries[col] * a.I * 3 + (row >> 3) * 24 + (row & 7);
+      const __bf16 h0 = (__bf16)h;
+      const float r1 = h - (float)h0;
+      const __bf16 h1 = (__bf16)r1;
+      const __bf16 h2 = (__bf16)(r1 - (float)h1);
+      a.h[at] = __builtin_bit_cast(uint16_t, h0);
+      a.h[at + 8] = __builtin_bit_cast(uint16_t, h1);
+      a.h[at + 16] = __builtin_bit_cast(uint16_t, h2);
+    }
+    ++done;
+  };
 #pragma unroll
   for (int i = 0; i < TI; ++i) acc[0][0][i] = acc[1][0][i] = 0.f;
-  if (n_it > 0) {
+  if (rt == tiles) {                                  // more waves than column blocks
+    for (int t = 0; t < tiles; ++t) finish();
+  } else {
     Block b[D];
 #pragma unroll
-    for (int d = 0; d < D - 1; ++d) load(b[d], d);
-    for (int i0 = 0; i0 < n_it; i0 += D) {
+    for (int d = 0; d < D - 1; ++d) load(b[d]);
+    for (bool more = true; more;) {
 #pragma unroll
       for (int d = 0; d < D; ++d) {
-        if (i0 + d >= n_it) break;
-        load(b[(d + D - 1) % D], i0 + d + D - 1);
+        if (!__builtin_amdgcn_readfirstlane(b[d].valid)) {
+          more = false;
+          break;
+        }
+        load(b[(d + D - 1) % D]);
         mul_tiles<2, 1, TI, G, false>(acc, b[d].t, b[d].x);
+        if (__builtin_amdgcn_readfirstlane(b[d].flush)) finish();
       }
     }
   }
-  __syncthreads();                                    // the previous columns' sums are read
-#pragma unroll
-  for (int i = 0; i < TI; ++i) {
-    red[0][i][wave][lane] = acc[0][0][i];
-    red[1][i][wave][lane] = acc[1][0][i];
-  }
-  __syncthreads();
-  for (int id = threadIdx.x; id < TI * 64; id += kGuWaves * 64) {
-    const int l = id & 63, i = id >> 6;
-    float g = 0.f, u = 0.f;
-#pragma unroll
-    for (int s = 0; s < kGuWaves; ++s) {
-      g += red[0][i][s][l];
-      u += red[1][i][s][l];
-    }
-    const int col = result_token(l, i);
-    if (col >= n_cols) continue;
-    const float h = g / (1.f + expf(-g)) * u;
-    // h as three BF16 parts, all 24 bits of it: y keeps fp32's accuracy rather
-    // than BF16's.  Laid out [entry][8 of I][part][8], as four
-    // neighbouring lanes of the down product read it.
-    const int row = 16 * tile + (l & 15);
-    const int64_t at = (int64_t)entries[col] * a.I * 3 + (row >> 3) * 24 + (row & 7);
-    const __bf16 h0 = (__bf16)h;
-    const float r1 = h - (float)h0;
-    const __bf16 h1 = (__bf16)r1;
-    const __bf16 h2 = (__bf16)(r1 - (float)h1);
-    a.h[at] = __builtin_bit_cast(uint16_t, h0);
-    a.h[at + 8] = __builtin_bit_cast(uint16_t, h1);
-    a.h[at + 16] = __builtin_bit_cast(uint16_t, h2);
-  }
+  __syncthreads();                                    // before the next columns' sums
 }
 
 template <int G, bool SMALL>
-__global__ __launch_bounds__(kGuWaves * 64, 4) void q4_gate_up_kernel(Q4Experts a, bool clear_y) {
-  __shared__ float red[2][4][kGuWaves][64];
+__global__ __launch_bounds__(kGuWaves * 64, 4) void q4_gate_up_kernel(Q4Experts a, int per, bool clear_y) {
+  __shared__ float red[2][2][4][kGuWaves][64];
   __shared__ UnitList list;
   if (clear_y) {
     const int64_t all = (int64_t)gridDim.x * gridDim.y * kGuWaves * 64;
@@ -230,11 +256,12 @@ __global__ __launch_bounds__(kGuWaves * 64, 4) void q4_gate_up_kernel(Q4Experts 
   const int slot = __builtin_amdgcn_readfirstlane(u.x);
   const int count = __builtin_amdgcn_readfirstlane(u.z);
   const uint8_t* block = slot < 0 ? a.shared : a.pool + (int64_t)slot * a.expert_bytes;
+  const int tile = blockIdx.x * per, tiles = min(per, a.I / 16 - tile);
   for (int c0 = 0; c0 < count; c0 += 16) {
     const int n = min(16, count - c0);
-    if (n <= 4) gate_up_columns<1, G>(a, block, blockIdx.x, entries + c0, n, red);
-    else if (n <= 8) gate_up_columns<2, G>(a, block, blockIdx.x, entries + c0, n, red);
-    else gate_up_columns<4, G>(a, block, blockIdx.x, entries + c0, n, red);
+    if (n <= 4) gate_up_columns<1, G>(a, block, tile, tiles, entries + c0, n, red);
+    else if (n <= 8) gate_up_columns<2, G>(a, block, tile, tiles, entries + c0, n, red);
+    else gate_up_columns<4, G>(a, block, tile, tiles, entries + c0, n, red);
   }
 }
 
@@ -254,8 +281,8 @@ __global__ __launch_bounds__(kGuWaves * 64, 4) void q4_gate_up_kernel(Q4Experts 
 // l / 16.
 //
 // Bound: the loads of h (64 bytes of an entry for every 16 bytes of codes that
-// meet them) beside the experts' bytes.  The cases of the gate / up product: 35 us,
-// 3.4 TB/s; 6 us; 45 us, 2.3 TB/s.
+// meet them) beside the experts' bytes.  The cases of the gate / up product: 33 us,
+// 3.6 TB/s; 6 us; 41 us, 2.5 TB/s.
 constexpr int kDnWaves = 16;
 
 template <int G, bool SMALL>
@@ -414,12 +441,17 @@ int down_split(const Q4Experts& a) { return a.H / 16 <= 128 ? 2 : 1; }
 template <int G, bool SMALL>
 hipError_t run_products(const Q4Experts& a, hipStream_t st) {
   const int most = (a.P < a.E ? a.P : a.E) + (a.shared ? 1 : 0);   // units at most
-  hipLaunchKernelGGL((q4_gate_up_kernel<G, SMALL>), dim3(a.I / 16, most), dim3(kGuWaves * 64), 0,
-                     st, a, down_split(a) > 1);
+  const int tiles = a.I / 16 * most;
+  // The compute units hold 1024 workgroups of gate / up.  Twice that many and more
+  // take two row tiles each: 64 tokens of 2048/768, 6144 tiles, 53 -> 51 us; 3200
+  // tiles the same; 384 7 -> 9 us.
+  const int per = tiles >= 2048 ? 2 : 1;
+  hipLaunchKernelGGL((q4_gate_up_kernel<G, SMALL>), dim3((a.I / 16 + per - 1) / per, most),
+                     dim3(kGuWaves * 64), 0, st, a, per, down_split(a) > 1);
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  // enough jobs for four rounds of the waves: an uneven last one costs little
   const int split = down_split(a);
+  // enough jobs for four rounds of the waves: an uneven last one costs little
   int cut = (4 * kDnWaves * split + most - 1) / most;
   const int nkb = (a.I + 127) / 128;
   cut = cut < 1 ? 1 : cut > nkb ? nkb : cut;
