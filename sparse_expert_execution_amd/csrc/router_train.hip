@@ -371,6 +371,14 @@ __device__ __forceinline__ void router_dx(const float* __restrict__ dz,
   const int nks = (E + 31) / 32, nc = (H + 63) / 64;
   const int64_t t0 = (int64_t)bx * 16 * NTL;
   const bool vec = E % 4 == 0;
+  // W of the first chunk, on its way while dz is staged; from then on always the
+  // next 32 experts', into the next chunk
+  const int step = ny * kDxWaves;
+  int c = by * kDxWaves + wave;
+  const u32x4* src = wf + (int64_t)(c < nc ? c : 0) * nks * 4 * PL * 64 + lane;
+  u32x4 a[4 * PL];
+#pragma unroll
+  for (int i = 0; i < 4 * PL; ++i) a[i] = src[i * 64];
   // four pieces' loads in flight before the first is used
   for (int i0 = wave; i0 < nks * NTL; i0 += 4 * kDxWaves) {
     float v[4][8];
@@ -410,21 +418,18 @@ __device__ __forceinline__ void router_dx(const float* __restrict__ dz,
     }
   }
   __syncthreads();
-  for (int c = by * kDxWaves + wave; c < nc; c += ny * kDxWaves) {
+  for (; c < nc; c += step) {
     v4f acc[4][NTL];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int t = 0; t < NTL; ++t) acc[j][t] = v4f{0.f, 0.f, 0.f, 0.f};
-    const u32x4* src = wf + (int64_t)c * nks * 4 * PL * 64 + lane;
-    u32x4 a[4 * PL];
-#pragma unroll
-    for (int i = 0; i < 4 * PL; ++i) a[i] = src[i * 64];
     for (int ks = 0; ks < nks; ++ks) {
       u32x4 an[4 * PL];
-      const u32x4* nsrc = src + (int64_t)(ks + 1 < nks ? ks + 1 : ks) * 4 * PL * 64;
+      if (ks + 1 < nks) src += 4 * PL * 64;
+      else if (c + step < nc) src += ((int64_t)(step - 1) * nks + 1) * 4 * PL * 64;
 #pragma unroll
-      for (int i = 0; i < 4 * PL; ++i) an[i] = nsrc[i * 64];
+      for (int i = 0; i < 4 * PL; ++i) an[i] = src[i * 64];
 #pragma unroll
       for (int t = 0; t < NTL; ++t) {
         const u32x4 hi = sb[((ks * NTL + t) * 2) * 64 + lane];
