@@ -358,7 +358,7 @@ __global__ __launch_bounds__(256) void pack_kernel(const void* __restrict__ w,
 // operand without reuse in a workgroup, comes from the L2 in operand order.
 //
 // Bound: the matrix cores, 2 T H E operations for each part of dz (three pairs of
-// parts where W is fp32).  T = 16384, H = 4096, E = 256: 75 us, 0.92 PFLOP/s.
+// parts where W is fp32).  T = 16384, H = 4096, E = 256: 72 us, 0.95 PFLOP/s.
 constexpr int kDxWaves = 8;
 
 template <int NTL, bool RF32>
@@ -474,7 +474,7 @@ __device__ __forceinline__ void router_dx(const float* __restrict__ dz,
 // h = 4 n + f, so a lane ends up with four consecutive h of a row.
 //
 // Bound: the matrix cores, three times 2 T H E operations.  T = 16384, H = 4096, E
-// = 256: 96 us, 1.07 PFLOP/s, and 11 us for the sum over 16 slices of tokens.
+// = 256: 94 us, 1.09 PFLOP/s, and 11 us for the sum over 16 slices of tokens.
 constexpr int kDwWaves = 8, kDwH = 64 * kDwWaves;
 
 __device__ __forceinline__ uint32_t pack_lo(uint32_t a, uint32_t b) {
@@ -498,19 +498,24 @@ __device__ __forceinline__ void router_dw(const uint16_t* __restrict__ x,
   const bool hin = h < H;
   const u32x4* zsrc = zf + (int64_t)by * ET * kZp * 64;
 
+  // The next step's loads, none of them behind a branch: rows past the last token
+  // read the last one (dz is packed with zeros there, and what that row does to a
+  // sum of its column it does anyway), a step past the slice its last step.  (Two
+  // steps ahead in short batches: no change.)
   u32x4 za[kCopies];
   uint2 xr[8];
-  auto load = [&](int kt) {
+  const uint16_t* xh = x + (hin ? h : 0);
+  auto load = [&](int step) {
+    const int kt = min(step, k1 - 1);
 #pragma unroll
     for (int c = 0; c < kCopies; ++c) {
       const int i = c * kDwWaves * 64 + threadIdx.x;
-      if (i < kStage) za[c] = zsrc[(int64_t)kt * net * kZp * 64 + i];
+      za[c] = zsrc[(int64_t)kt * net * kZp * 64 + min(i, kStage - 1)];
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int64_t t = 32 * (int64_t)kt + 8 * q + i;
-      xr[i] = make_uint2(0, 0);
-      if (t < T && hin) xr[i] = *reinterpret_cast<const uint2*>(x + t * H + h);
+      const int64_t t = min(32 * kt + 8 * q + i, T - 1);
+      xr[i] = *reinterpret_cast<const uint2*>(xh + t * H);
     }
   };
   auto stage = [&](int b) {
@@ -538,7 +543,7 @@ __device__ __forceinline__ void router_dw(const uint16_t* __restrict__ x,
       b[2][i] = pack_lo(xr[2 * i].y, xr[2 * i + 1].y);
       b[3][i] = pack_hi(xr[2 * i].y, xr[2 * i + 1].y);
     }
-    if (kt + 1 < k1) load(kt + 1);
+    load(kt + 1);
     const int buf = (kt - k0) & 1;
     __syncthreads();                                  // this step's dz is in LDS
 #pragma unroll
@@ -551,7 +556,7 @@ __device__ __forceinline__ void router_dw(const uint16_t* __restrict__ x,
       }
     }
     // the other buffer was last read a step ago, before this step's barrier
-    if (kt + 1 < k1) stage(buf ^ 1);
+    stage(buf ^ 1);
   }
   if (!hin) return;
   float* o = out + (int64_t)bz * E * H;
