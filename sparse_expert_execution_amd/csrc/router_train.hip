@@ -474,7 +474,10 @@ __device__ __forceinline__ void router_dx(const float* __restrict__ dz,
 // h = 4 n + f, so a lane ends up with four consecutive h of a row.
 //
 // Bound: the matrix cores, three times 2 T H E operations.  T = 16384, H = 4096, E
-// = 256: 94 us, 1.09 PFLOP/s, and 11 us for the sum over 16 slices of tokens.
+// = 256: 92 us, 1.12 PFLOP/s, and 11 us for the sum over 16 slices of tokens.
+// The slices run fastest over the workgroups: where their number is a multiple of
+// 8, the workgroups of one, which share its dz and x, are on one XCD (160 MB
+// fetched; with the chunks of h fastest, every XCD took all of dz: 336 MB, 2 us).
 constexpr int kDwWaves = 8, kDwH = 64 * kDwWaves;
 
 __device__ __forceinline__ uint32_t pack_lo(uint32_t a, uint32_t b) {
@@ -583,7 +586,7 @@ __global__ __launch_bounds__(kDwWaves * 64, 2) void router_dw_kernel(const uint1
                                                                      const u32x4* zf, int T,
                                                                      int H, int E, int net,
                                                                      int per_slice, float* out) {
-  router_dw<ET>(x, zf, T, H, E, net, per_slice, out, blockIdx.x, blockIdx.y, blockIdx.z);
+  router_dw<ET>(x, zf, T, H, E, net, per_slice, out, blockIdx.y, blockIdx.z, blockIdx.x);
 }
 
 // Both in one launch, where neither fills the chip: workgroups 0 .. ndx - 1 are
@@ -684,7 +687,7 @@ hipError_t run_dx(const RouterBackward& a, const DxPlan& p, const u32x4* wf, hip
 template <int ET>
 hipError_t run_dw(const RouterBackward& a, const DwPlan& p, const u32x4* zf, float* out,
                   hipStream_t st) {
-  const dim3 g((a.H + kDwH - 1) / kDwH, p.net / p.et, p.slices);
+  const dim3 g(p.slices, (a.H + kDwH - 1) / kDwH, p.net / p.et);
   hipLaunchKernelGGL(router_dw_kernel<ET>, g, dim3(kDwWaves * 64), 0, st,
                      static_cast<const uint16_t*>(a.x), zf, a.T, a.H, a.E, p.net, p.per_slice, out);
   return hipGetLastError();
