@@ -400,3 +400,64 @@ def test_a_training_step_in_a_graph(ops):
         torch.cuda.synchronize()
         for n in ("ids", "w", "counts", "loss", "dz", "dx", "dwr"):
             assert torch.equal(a[n], b[n]), n
+
+
+def test_two_streams_and_two_graphs_on_one_workspace(ops):
+    """Calls at once on two streams, each with workspaces of its own, and two graphs
+    that share a workspace and are replayed in turn, with eager calls between."""
+    T, H, E, k = 777, 512, 128, 8
+    desc = ops.make_desc(H, 256, E, k, router_wtype="f32")
+    sets = []
+    for seed in (51, 52):
+        x, w, _ = _router_inputs(T, H, E, "f32", seed)
+        b = dict(x=x, w=w, z=torch.empty((T, E), device="cuda"),
+                 ids=torch.empty((T, k), dtype=torch.int32, device="cuda"),
+                 gw=torch.empty((T, k), device="cuda"),
+                 counts=torch.empty(E + 1, dtype=torch.int32, device="cuda"),
+                 loss=torch.empty(1, device="cuda"), dz=torch.empty((T, E), device="cuda"),
+                 dx=torch.empty((T, H), dtype=torch.bfloat16, device="cuda"),
+                 dw=torch.empty((E, H), device="cuda"),
+                 dgw=torch.randn((T, k), device="cuda"), one=torch.ones(1, device="cuda"),
+                 ws=ops.workspace(desc, T, ops.MODE_GATE),
+                 rws=ops.workspace(desc, T, ops.MODE_ROUTER_BACKWARD))
+        sets.append(b)
+
+    def step(b, ws, rws, stream=None):
+        ops.router_logits(desc, b["x"], b["w"], b["z"], stream=stream)
+        ops.gate(desc, b["z"], b["ids"], b["gw"], ws, counts=b["counts"], loss=b["loss"],
+                 stream=stream)
+        ops.gate_backward(desc, b["z"], b["ids"], b["gw"], b["dz"], dw=b["dgw"],
+                          counts=b["counts"], dloss=b["one"], stream=stream)
+        ops.router_backward(desc, b["x"], b["w"], b["dz"], rws, dx=b["dx"], dw_router=b["dw"],
+                            stream=stream)
+    outs = ("z", "ids", "gw", "counts", "loss", "dz", "dx", "dw")
+    want = []
+    for b in sets:
+        step(b, b["ws"], b["rws"])
+        torch.cuda.synchronize()
+        want.append({n: b[n].clone() for n in outs})
+
+    def check():
+        torch.cuda.synchronize()
+        for b, ref in zip(sets, want):
+            for n in outs:
+                assert torch.equal(b[n], ref[n]), n
+                b[n].zero_()
+    check()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        for b, st in zip(sets, streams):
+            step(b, b["ws"], b["rws"], stream=st)
+    check()
+    graphs = []
+    for b in sets:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step(b, sets[0]["ws"], sets[0]["rws"])
+        graphs.append(g)
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+        step(sets[0], sets[0]["ws"], sets[0]["rws"])
+        check()
