@@ -266,7 +266,7 @@ __global__ __launch_bounds__(kGuWaves * 64, 4) void q4_gate_up_kernel(Q4Experts 
 }
 
 // ---- down + combine -----------------------------------------------------------
-// One workgroup per 16 rows of y, for all tokens and experts, so the combine
+// One workgroup per 16 RT rows of y, for all tokens and experts, so the combine
 // needs no other pass: the units' tiles are cut into jobs (an item, i.e. up to
 // four entries of a unit, and a slice of I) that go round the 16 waves; a wave
 // adds a job's gate-weighted result into a y tile of its own in LDS, and the 16
@@ -281,15 +281,15 @@ __global__ __launch_bounds__(kGuWaves * 64, 4) void q4_gate_up_kernel(Q4Experts 
 // l / 16.
 //
 // Bound: the loads of h (64 bytes of an entry for every 16 bytes of codes that
-// meet them) beside the experts' bytes.  The cases of the gate / up product: 33 us,
-// 3.6 TB/s; 6 us; 41 us, 2.5 TB/s.
+// meet them; half of it with RT = 2) beside the experts' bytes.  The cases of the
+// gate / up product: 30 us, 4.0 TB/s (RT = 1: 33); 6 us; 41 us, 2.5 TB/s.
 constexpr int kDnWaves = 16;
 
-template <int G, bool SMALL>
+template <int RT, int G, bool SMALL>
 __global__ __launch_bounds__(kDnWaves * 64, 4) void q4_down_kernel(Q4Experts a, int cut) {
   constexpr int D = 3;
   constexpr int kPairs = SMALL ? kWavePairs : kQ4MaxPairs;
-  extern __shared__ float yl[];                       // [wave][T][16]
+  extern __shared__ float yl[];                       // [wave][T][16 RT]
   __shared__ UnitList list;
   __shared__ int4 s_unit[SMALL ? 1 : kPairs + 1];
   __shared__ int16_t s_entry[SMALL ? 1 : kPairs + kQ4MaxTokens];
@@ -302,7 +302,7 @@ __global__ __launch_bounds__(kDnWaves * 64, 4) void q4_down_kernel(Q4Experts a, 
     s_token[i] = (uint8_t)(i < a.P ? i / a.k : i - a.P);
     s_w[i] = i < a.P ? a.w[i] : 1.f;
   }
-  for (int j = threadIdx.x; j < kDnWaves * a.T * 16; j += kDnWaves * 64) yl[j] = 0.f;
+  for (int j = threadIdx.x; j < kDnWaves * a.T * 16 * RT; j += kDnWaves * 64) yl[j] = 0.f;
   int n_units;
   const int4* units;
   const int16_t* entries;
@@ -336,10 +336,10 @@ __global__ __launch_bounds__(kDnWaves * 64, 4) void q4_down_kernel(Q4Experts a, 
   }
   __syncthreads();
   const int n_items = __builtin_amdgcn_readfirstlane(s_items);
-  const int nkb = (a.I + 127) / 128, tile = blockIdx.x;
+  const int nkb = (a.I + 127) / 128, tile = blockIdx.x * RT;
   const int per = (nkb + cut - 1) / cut;              // column blocks of a job
   const int slices = (nkb + per - 1) / per;
-  float* mine = yl + (int64_t)wave * a.T * 16;
+  float* mine = yl + (int64_t)wave * a.T * 16 * RT;
   const int e4 = n >> 2, part = n & 3;                // as an operand row
 
   // Where the loads are: item `ii`, slice `sl` of its columns, column block kb.
@@ -368,7 +368,7 @@ __global__ __launch_bounds__(kDnWaves * 64, 4) void q4_down_kernel(Q4Experts a, 
 
   // a column block in flight; at the last one of a job: its entries and number
   struct Block {
-    Tile<G, false> t[1];
+    Tile<G, false> t[RT];
     bf16x8 x[1][4];
     int valid, flush, at;
   };
@@ -379,7 +379,8 @@ __global__ __launch_bounds__(kDnWaves * 64, 4) void q4_down_kernel(Q4Experts a, 
     b.valid = in;
     const uint8_t* block = slot < 0 ? a.shared : a.pool + (int64_t)uni(slot) * a.expert_bytes;
     const Matrix m{block + a.off[4], block + a.off[5], nullptr, nkb};
-    load_tile<G, false>(b.t[0], m, tile, kb, in);
+#pragma unroll
+    for (int r = 0; r < RT; ++r) load_tile<G, false>(b.t[r], m, tile + r, kb, in);
     load_rows<192>(b.x[0], hb, hrow, 768 * kb, in ? a.I - 128 * kb : 0);
     b.flush = 0;
     b.at = first;
@@ -401,7 +402,7 @@ __global__ __launch_bounds__(kDnWaves * 64, 4) void q4_down_kernel(Q4Experts a, 
     Block b[D];
 #pragma unroll
     for (int d = 0; d < D - 1; ++d) load(b[d]);
-    float acc[1][1][3] = {};
+    float acc[RT][1][3] = {};
     for (bool more = true; more;) {
 #pragma unroll
       for (int d = 0; d < D; ++d) {
@@ -410,33 +411,47 @@ __global__ __launch_bounds__(kDnWaves * 64, 4) void q4_down_kernel(Q4Experts a, 
           break;
         }
         load(b[(d + D - 1) % D]);
-        mul_tiles<1, 1, 3, G, false>(acc, b[d].t, b[d].x);
+        mul_tiles<RT, 1, 3, G, false>(acc, b[d].t, b[d].x);
         const int flush = uni(b[d].flush);
         if (flush == 0) continue;
         if (q < flush) {
           const int e = entries[b[d].at + q];
           // an LDS add: a token that names one expert twice is two entries here
-          __hip_atomic_fetch_add(&mine[s_token[e] * 16 + n],
-                                 s_w[e] * (acc[0][0][0] + (acc[0][0][1] + acc[0][0][2])),
-                                 __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+#pragma unroll
+          for (int r = 0; r < RT; ++r)
+            __hip_atomic_fetch_add(&mine[(s_token[e] * RT + r) * 16 + n],
+                                   s_w[e] * (acc[r][0][0] + (acc[r][0][1] + acc[r][0][2])),
+                                   __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
         }
-        acc[0][0][0] = acc[0][0][1] = acc[0][0][2] = 0.f;
+#pragma unroll
+        for (int r = 0; r < RT; ++r) acc[r][0][0] = acc[r][0][1] = acc[r][0][2] = 0.f;
       }
     }
   }
   __syncthreads();
-  for (int j = threadIdx.x; j < a.T * 16; j += kDnWaves * 64) {
+  for (int j = threadIdx.x; j < a.T * 16 * RT; j += kDnWaves * 64) {
     float v = 0.f;
 #pragma unroll
-    for (int s = 0; s < kDnWaves; ++s) v += yl[(int64_t)s * a.T * 16 + j];
-    float* y = a.y + (int64_t)(j >> 4) * a.H + 16 * tile + (j & 15);
+    for (int s = 0; s < kDnWaves; ++s) v += yl[(int64_t)s * a.T * 16 * RT + j];
+    float* y = a.y + (int64_t)(j / (16 * RT)) * a.H + 16 * tile + j % (16 * RT);
     if (gridDim.y == 1) *y = v;
     else __hip_atomic_fetch_add(y, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
 }
 
-// workgroups that share a tile of y (two: y is cleared by the gate / up launch)
-int down_split(const Q4Experts& a) { return a.H / 16 <= 128 ? 2 : 1; }
+// Row tiles of a down workgroup: two, with half the loads of h for each, where that
+// still gives a workgroup for every second compute unit (H is a multiple of 32).
+int down_tiles(const Q4Experts& a) { return a.H / 32 >= 128 ? 2 : 1; }
+// workgroups that share them (two: y is cleared by the gate / up launch)
+int down_split(const Q4Experts& a) { return a.H / (16 * down_tiles(a)) <= 128 ? 2 : 1; }
+
+template <int RT, int G, bool SMALL>
+hipError_t run_down(const Q4Experts& a, int cut, hipStream_t st) {
+  hipLaunchKernelGGL((q4_down_kernel<RT, G, SMALL>), dim3(a.H / (16 * RT), down_split(a)),
+                     dim3(kDnWaves * 64), (size_t)kDnWaves * a.T * 16 * RT * sizeof(float), st, a,
+                     cut);
+  return hipGetLastError();
+}
 
 template <int G, bool SMALL>
 hipError_t run_products(const Q4Experts& a, hipStream_t st) {
@@ -455,9 +470,7 @@ hipError_t run_products(const Q4Experts& a, hipStream_t st) {
   int cut = (4 * kDnWaves * split + most - 1) / most;
   const int nkb = (a.I + 127) / 128;
   cut = cut < 1 ? 1 : cut > nkb ? nkb : cut;
-  hipLaunchKernelGGL((q4_down_kernel<G, SMALL>), dim3(a.H / 16, split), dim3(kDnWaves * 64),
-                     (size_t)kDnWaves * a.T * 16 * sizeof(float), st, a, cut);
-  return hipGetLastError();
+  return down_tiles(a) == 2 ? run_down<2, G, SMALL>(a, cut, st) : run_down<1, G, SMALL>(a, cut, st);
 }
 
 template <int G>
