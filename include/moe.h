@@ -254,8 +254,9 @@ int moe_router_backward(const moe_desc* desc, const void* x, const void* w_route
  * atomic, so the summation order (and the last bits of y) can differ
  * between runs.  INT4 experts: x as given, h in fp32 (handed on as three BF16
  * parts), fp32 accumulation, all T tokens in one pass, no wait between
- * workgroups, and equal calls give equal bits: at most two workgroups add into
- * an element of y, which is cleared first (0 + a + b).  x is taken to be below
+ * workgroups, and equal calls give equal bits (at most two workgroups add into
+ * an element of y, which is cleared first, 0 + a + b; the sums of more are added
+ * in a fixed order).  x is taken to be below
  * 2^120 in magnitude; an infinity in it, or an h that overflows, makes the
  * token's y NaN.
  *   x              device [T][H] BF16;   1 <= T <= MOE_DECODE_MAX_T

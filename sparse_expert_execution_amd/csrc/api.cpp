@@ -86,9 +86,9 @@ RouteWs route_ws(const moe_desc* d, int T, bool decode) {
 // decode workspace of 4-bit integer experts: the header (the router's ticket
 // is its first word), logits z [T][E], the number of units, the units and
 // their entries, h of every pair and of the shared expert's tokens in three
-// BF16 parts.
+// BF16 parts, partial sums of y.
 struct Q4DecodeWs {
-  size_t z, n_units, units, entries, h, total;
+  size_t z, n_units, units, entries, h, part, total;
 };
 Q4DecodeWs q4_decode_ws(const moe_desc* d, int T) {
   Q4DecodeWs w;
@@ -99,6 +99,7 @@ Q4DecodeWs q4_decode_ws(const moe_desc* d, int T) {
   w.units = o; o = align_up(o + (P + 1) * 16);
   w.entries = o; o = align_up(o + (P + T) * 2);
   w.h = o; o = align_up(o + (P + T) * d->inter * 6);
+  w.part = o; o = align_up(o + (size_t)moe::q4_down_parts((int)P, d->hidden) * T * d->hidden * 4);
   w.total = o;
   return w;
 }
@@ -243,6 +244,7 @@ static int q4_decode_impl(const moe_desc* desc, const void* x, const void* w_rou
   a.units = reinterpret_cast<int4*>(b + L.units);
   a.entries = reinterpret_cast<int16_t*>(b + L.entries);
   a.h = reinterpret_cast<uint16_t*>(b + L.h);
+  a.part = reinterpret_cast<float*>(b + L.part);
   return hip_status(moe::launch_q4_experts(a, moe::q4_group(desc->wtype), as_stream(stream)),
                     name);
 }

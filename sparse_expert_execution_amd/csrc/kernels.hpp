@@ -167,7 +167,20 @@ struct Q4Experts {
   int16_t* entries;        // [P + T] pair numbers, P + t for the shared expert
   uint16_t* h;             // [P + T][I / 8][4][8] h as three BF16 parts (the fourth unused)
   int P;                   // set by the launcher
+  float* part;             // [q4_down_parts][T][H], where there are any
 };
+// Workgroups that share rows of y in the down product of more pairs than one wave
+// lists (kQ4WavePairs): 32 rows for each, one workgroup per compute unit, at most 8
+// sharing.  More than two of them leave partial sums, added in order by one more
+// launch (two add into a cleared y: that has one order).
+constexpr int kQ4WavePairs = 64;
+inline int q4_down_split(int H) {
+  const int s = 256 / (H / 32);
+  return s < 1 ? 1 : s > 8 ? 8 : s;
+}
+inline int q4_down_parts(int pairs, int H) {
+  return pairs > kQ4WavePairs && q4_down_split(H) > 2 ? q4_down_split(H) : 0;
+}
 hipError_t launch_q4_experts(Q4Experts a, int group, hipStream_t st);
 
 // per-workgroup phase stamps at the end of the decode workspace

@@ -75,7 +75,7 @@ __global__ __launch_bounds__(kUnitThreads) void q4_units_kernel(Q4Experts a) {
 }
 
 // The same list of at most 64 pairs by one wave, into LDS.  Lane i is pair i.
-constexpr int kWavePairs = 64;
+constexpr int kWavePairs = kQ4WavePairs;
 
 struct UnitList {
   int4 unit[kWavePairs + 1];
@@ -270,19 +270,20 @@ __global__ __launch_bounds__(kGuWaves * 64, 4) void q4_gate_up_kernel(Q4Experts 
 // needs no other pass: the units' tiles are cut into jobs (an item, i.e. up to
 // four entries of a unit, and a slice of I) that go round the 16 waves; a wave
 // adds a job's gate-weighted result into a y tile of its own in LDS, and the 16
-// tiles are summed in wave order.  Where that gives workgroups for half the
-// compute units at most, two share the jobs of a tile and add into a cleared y:
-// 0 + a + b has one value whichever comes first.
+// tiles are summed in wave order.  Where that gives too few workgroups for the
+// compute units, several share the jobs of a tile: two add into a cleared y (0 + a
+// + b has one value whichever comes first), more leave their sums to one more
+// launch that adds them in order.
 //
 // Operand row 4 e + part is part `part` of h of the job's entry e (the fourth row
-// of an entry is empty), so one instruction takes four entries, four neighbouring
-// lanes of a load read 64 bytes of one entry (rows of h apart from each other were
-// a cache access per lane), and a lane's results 0, 1, 2 are the parts of entry
+// of an entry is empty), so one instruction takes four entries, neighbouring lanes
+// of a load read 48 bytes of one entry (rows of h apart from each other were a
+// cache access per lane), and a lane's results 0, 1, 2 are the parts of entry
 // l / 16.
 //
-// Bound: the loads of h (64 bytes of an entry for every 16 bytes of codes that
-// meet them; half of it with RT = 2) beside the experts' bytes.  The cases of the
-// gate / up product: 30 us, 4.0 TB/s (RT = 1: 33); 6 us; 41 us, 2.5 TB/s.
+// Bound: the loads of h (an item of four entries reads 3 KB of it for each 1 KB of
+// codes, half of that with RT = 2) beside the experts' bytes.  The cases of the
+// gate / up product: 30 us, 4.0 TB/s (RT = 1: 33); 6 us; 35 us, 3.0 TB/s.
 constexpr int kDnWaves = 16;
 
 template <int RT, int G, bool SMALL>
@@ -434,22 +435,43 @@ __global__ __launch_bounds__(kDnWaves * 64, 4) void q4_down_kernel(Q4Experts a, 
 #pragma unroll
     for (int s = 0; s < kDnWaves; ++s) v += yl[(int64_t)s * a.T * 16 * RT + j];
     float* y = a.y + (int64_t)(j / (16 * RT)) * a.H + 16 * tile + j % (16 * RT);
-    if (gridDim.y == 1) *y = v;
+    if (a.part) a.part[(int64_t)blockIdx.y * a.T * a.H + (y - a.y)] = v;
+    else if (gridDim.y == 1) *y = v;
     else __hip_atomic_fetch_add(y, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
 }
 
+// y = the sum of the workgroups' shares, in their order
+__global__ __launch_bounds__(256) void q4_sum_kernel(const float* part, int parts, int n, float* y) {
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= n) return;
+  float s = part[i];
+  for (int p = 1; p < parts; ++p) s += part[(int64_t)p * n + i];
+  y[i] = s;
+}
+
 // Row tiles of a down workgroup: two, with half the loads of h for each, where that
-// still gives a workgroup for every second compute unit (H is a multiple of 32).
-int down_tiles(const Q4Experts& a) { return a.H / 32 >= 128 ? 2 : 1; }
+// still gives a workgroup for every second compute unit (H is a multiple of 32), and
+// for many pairs, where h is most of what is loaded: 64 tokens of 2048/768 35 us and
+// 5 of q4_sum_kernel, the call 92 us; one row tile and no such launch 42, 97.
+template <bool SMALL>
+int down_tiles(const Q4Experts& a) { return !SMALL || a.H / 32 >= 128 ? 2 : 1; }
 // workgroups that share them (two: y is cleared by the gate / up launch)
-int down_split(const Q4Experts& a) { return a.H / (16 * down_tiles(a)) <= 128 ? 2 : 1; }
+template <bool SMALL>
+int down_split(const Q4Experts& a) {
+  return !SMALL ? q4_down_split(a.H) : a.H / (16 * down_tiles<SMALL>(a)) <= 128 ? 2 : 1;
+}
 
 template <int RT, int G, bool SMALL>
 hipError_t run_down(const Q4Experts& a, int cut, hipStream_t st) {
-  hipLaunchKernelGGL((q4_down_kernel<RT, G, SMALL>), dim3(a.H / (16 * RT), down_split(a)),
+  hipLaunchKernelGGL((q4_down_kernel<RT, G, SMALL>), dim3(a.H / (16 * RT), down_split<SMALL>(a)),
                      dim3(kDnWaves * 64), (size_t)kDnWaves * a.T * 16 * RT * sizeof(float), st, a,
                      cut);
+  const hipError_t err = hipGetLastError();
+  if (err != hipSuccess || !a.part) return err;
+  const int n = a.T * a.H;
+  hipLaunchKernelGGL(q4_sum_kernel, dim3((n + 255) / 256), dim3(256), 0, st, a.part,
+                     down_split<SMALL>(a), n, a.y);
   return hipGetLastError();
 }
 
@@ -462,15 +484,17 @@ hipError_t run_products(const Q4Experts& a, hipStream_t st) {
   // tiles the same; 384 7 -> 9 us.
   const int per = tiles >= 2048 ? 2 : 1;
   hipLaunchKernelGGL((q4_gate_up_kernel<G, SMALL>), dim3((a.I / 16 + per - 1) / per, most),
-                     dim3(kGuWaves * 64), 0, st, a, per, down_split(a) > 1);
+                     dim3(kGuWaves * 64), 0, st, a, per, down_split<SMALL>(a) > 1 && !a.part);
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  const int split = down_split(a);
+  const int split = down_split<SMALL>(a);
   // enough jobs for four rounds of the waves: an uneven last one costs little
   int cut = (4 * kDnWaves * split + most - 1) / most;
   const int nkb = (a.I + 127) / 128;
   cut = cut < 1 ? 1 : cut > nkb ? nkb : cut;
-  return down_tiles(a) == 2 ? run_down<2, G, SMALL>(a, cut, st) : run_down<1, G, SMALL>(a, cut, st);
+  if constexpr (SMALL)
+    if (down_tiles<SMALL>(a) == 1) return run_down<1, G, SMALL>(a, cut, st);
+  return run_down<2, G, SMALL>(a, cut, st);
 }
 
 template <int G>
@@ -486,6 +510,7 @@ hipError_t run(const Q4Experts& a, hipStream_t st) {
 
 hipError_t launch_q4_experts(Q4Experts a, int group, hipStream_t st) {
   a.P = a.T * a.k;
+  if (!q4_down_parts(a.P, a.H)) a.part = nullptr;
   if (a.T < 1 || a.P > kQ4MaxPairs || a.T > kQ4MaxTokens) return hipErrorInvalidValue;
   if (group == 32) return run<32>(a, st);
   if (group == 64) return run<64>(a, st);

@@ -296,6 +296,7 @@ EXPERTS = [
     (32, 32, 1, 1, 32, False, 1), (256, 128, 8, 2, 128, False, 1), (800, 96, 20, 3, 32, True, 5),
     (512, 256, 12, 3, 64, True, 64), (96, 160, 5, 4, 128, True, 33), (2048, 768, 16, 8, 128, False, 1),
     (160, 1056, 40, 8, 64, False, 64), (1024, 64, 6, 6, 32, False, 17),
+    (2048, 64, 20, 3, 64, True, 64),
     # two row tiles a down workgroup; two of them, or one, for each
     (4096, 64, 24, 4, 64, True, 64), (4096, 160, 12, 3, 32, False, 3),
     (4128, 32, 5, 2, 128, False, 40), (8192, 64, 9, 2, 32, True, 2),
