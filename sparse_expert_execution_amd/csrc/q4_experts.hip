@@ -231,7 +231,8 @@ __device__ __forceinline__ void gate_up_columns(const Q4Experts& a, const uint8_
 }
 
 template <int G, bool SMALL>
-__global__ __launch_bounds__(kGuWaves * 64, 4) void q4_gate_up_kernel(Q4Experts a, int per, bool clear_y) {
+__global__ __launch_bounds__(kGuWaves * 64, 4) void q4_gate_up_kernel(Q4Experts a, int per,
+                                                                      bool clear_y) {
   __shared__ float red[2][2][4][kGuWaves][64];
   __shared__ UnitList list;
   if (clear_y) {
@@ -295,7 +296,7 @@ __global__ __launch_bounds__(kDnWaves * 64, 4) void q4_down_kernel(Q4Experts a, 
   __shared__ int4 s_unit[SMALL ? 1 : kPairs + 1];
   __shared__ int16_t s_entry[SMALL ? 1 : kPairs + kQ4MaxTokens];
   __shared__ float s_w[kPairs + kQ4MaxTokens];
-  __shared__ int s_item[kPairs + kQ4MaxTokens / 4], s_items;   // q4_items at most
+  __shared__ int s_item[kPairs + kQ4MaxTokens / 4], s_items;   // a pair each at most
   __shared__ uint8_t s_token[kPairs + kQ4MaxTokens];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 4, n = lane & 15;
   // by pair: the token and the gate weight
@@ -442,7 +443,8 @@ __global__ __launch_bounds__(kDnWaves * 64, 4) void q4_down_kernel(Q4Experts a, 
 }
 
 // y = the sum of the workgroups' shares, in their order
-__global__ __launch_bounds__(256) void q4_sum_kernel(const float* part, int parts, int n, float* y) {
+__global__ __launch_bounds__(256) void q4_sum_kernel(const float* part, int parts, int n,
+                                                     float* y) {
   const int i = blockIdx.x * 256 + threadIdx.x;
   if (i >= n) return;
   float s = part[i];
